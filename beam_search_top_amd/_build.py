@@ -32,6 +32,11 @@ KERNELS = os.path.join(CSRC, "rtopk_kernels.hip")
 HOST = os.path.join(CSRC, "rtopk_host.cpp")
 REORDER = os.path.join(CSRC, "rtopk_reorder.hip")
 SAMPLE = os.path.join(CSRC, "rtopk_sample.hip")
+PAGED = os.path.join(CSRC, "rtopk_paged.hip")
+ATTN = os.path.join(CSRC, "rtopk_attn.hip")
+LAYER = os.path.join(CSRC, "rtopk_layer.cpp")
+# the attention kernels have to keep what a NaN means: a masked one is dropped, another spreads
+ATTN_FLAGS = [f for f in FLAGS if f != "-fno-honor-nans"]
 NOALLOC = os.path.join(CSRC, "rtopk_noalloc.hip")
 DTYPES = (0, 1, 2)  # the kernel source is compiled once per logit type, in parallel
 
@@ -54,9 +59,12 @@ def _run(cmds, verbose):
 
 def build(verbose: bool = False, extra=()) -> str:
     tag = f".tmp{os.getpid()}"
-    objs = [LIB + f".dt{d}{tag}.o" for d in DTYPES] + [LIB + f".noalloc{tag}.o", LIB + f".sample{tag}.o",
-                                                       LIB + f".reorder{tag}.o", LIB + f".host{tag}.o"]
+    objs = [LIB + f".dt{d}{tag}.o" for d in DTYPES] + [LIB + f".{n}{tag}.o" for n in (
+        "attn", "paged", "layer", "noalloc", "sample", "reorder", "host")]
     cmds = [[HIPCC, *FLAGS, *extra, f"-DRTOPK_DTYPE={d}", "-c", KERNELS, "-o", o] for d, o in zip(DTYPES, objs)]
+    cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", ATTN, "-o", objs[-7]])
+    cmds.append([HIPCC, *FLAGS, *extra, "-c", PAGED, "-o", objs[-6]])
+    cmds.append([HIPCC, *FLAGS, *extra, "-c", LAYER, "-o", objs[-5]])
     cmds.append([HIPCC, *FLAGS, *extra, "-c", NOALLOC, "-o", objs[-4]])
     cmds.append([HIPCC, *FLAGS, *extra, "-c", SAMPLE, "-o", objs[-3]])
     cmds.append([HIPCC, *FLAGS, *extra, "-c", REORDER, "-o", objs[-2]])

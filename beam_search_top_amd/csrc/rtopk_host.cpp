@@ -7,6 +7,7 @@
 // inference article (its memory-reuse passage): buffers are sized once and
 // reused on every request instead of being allocated per step.
 #include "rtopk.h"
+#include "rtopk_attn.h"
 #include "rtopk_internal.h"
 
 #include <hip/hip_runtime_api.h>
@@ -349,13 +350,13 @@ struct WsEntry {
 std::mutex g_ws_mu;
 std::map<std::pair<int, void *>, WsEntry> g_ws;
 
-int acquire_workspace(size_t need, hipStream_t stream, void **out)
+// With g_ws_mu held.
+int acquire_locked(size_t need, hipStream_t stream, void **out)
 {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess)
         return fail(RTOPK_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
-    std::lock_guard<std::mutex> lock(g_ws_mu);
     WsEntry &w = g_ws[{dev, (void *)stream}];
     if (w.bytes < need) {
         if (w.ptr) {
@@ -384,6 +385,12 @@ int acquire_workspace(size_t need, hipStream_t stream, void **out)
     }
     *out = w.ptr;
     return RTOPK_OK;
+}
+
+int acquire_workspace(size_t need, hipStream_t stream, void **out)
+{
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    return acquire_locked(need, stream, out);
 }
 
 // A device buffer of zeros per device (the running scores of sampling rows),
@@ -420,6 +427,21 @@ int acquire_zeros(size_t n, hipStream_t stream, const float **out)
 }
 
 } // namespace
+
+int rtopk::with_workspace(size_t need, hipStream_t stream, const std::function<int(void *)> &launch)
+{
+    // a captured launch would keep the address of a buffer that a later call may free
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(stream, &cap);
+    if (e != hipSuccess)
+        return fail(RTOPK_EHIP, "hipStreamIsCapturing: %s", hipGetErrorString(e));
+    if (cap != hipStreamCaptureStatusNone)
+        return fail(RTOPK_EINVAL, "a captured call needs a workspace of the caller's");
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    void *ws = nullptr;
+    const int st = acquire_locked(need, stream, &ws);
+    return st == RTOPK_OK ? launch(ws) : st;
+}
 
 int rtopk::set_error(int status, const char *fmt, ...)
 {

@@ -91,6 +91,20 @@ def load():
     L.rtopk_lmhead_step.restype = i32
     L.rtopk_beam_reorder.argtypes = [vp, vp, ctypes.c_longlong, i32, i32, ctypes.c_longlong, vp, i32, vp]
     L.rtopk_beam_reorder.restype = i32
+    L.rtopk_page_tables.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp, vp]
+    L.rtopk_page_tables.restype = i32
+    L.rtopk_cache_store.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, i32, i32, vp]
+    L.rtopk_cache_store.restype = i32
+    L.rtopk_tree_attention.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, i32, i32, i32, i32, i32,
+                                       ctypes.c_float, vp, vp, vp, sz, vp]
+    L.rtopk_tree_attention.restype = i32
+    L.rtopk_tree_attention_workspace_bytes.argtypes = [i32] * 7
+    L.rtopk_tree_attention_workspace_bytes.restype = sz
+    L.rtopk_cross_attention.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                        ctypes.c_float, vp, vp, vp, sz, vp]
+    L.rtopk_cross_attention.restype = i32
+    L.rtopk_cross_attention_workspace_bytes.argtypes = [i32] * 6
+    L.rtopk_cross_attention_workspace_bytes.restype = sz
     L.rtopk_read_probe.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
     L.rtopk_read_probe.restype = i32
     L.rtopk_read_probe_shape.argtypes = [vp, sz, i32, i32, ctypes.c_uint32, vp, vp]
@@ -271,6 +285,40 @@ def rtopk_beam_reorder(src, dst, nslabs, B, beam, row_bytes, beam_ids, ld, strea
     return load().rtopk_beam_reorder(src, dst, nslabs, B, beam, row_bytes, beam_ids, ld, stream)
 
 
+def rtopk_page_tables(cache_lens, new_lens, B, page, free_pages, nfree, free_head, num_pages, table, table_ld, slots,
+                      positions, T, rows, cu_new, free_next, stream):
+    return load().rtopk_page_tables(cache_lens, new_lens, B, page, free_pages, nfree, free_head, num_pages, table,
+                                    table_ld, slots, positions, T, rows, cu_new, free_next, stream)
+
+
+def rtopk_cache_store(k, k_strides, v, v_strides, dtype, slots, T, Hkv, D, k_cache, v_cache, cache_strides, num_pages,
+                      page, stream):
+    """The stride arguments here and below are addresses of host int64 arrays (a ctypes array will do) or None."""
+    return load().rtopk_cache_store(k, k_strides, v, v_strides, dtype, slots, T, Hkv, D, k_cache, v_cache,
+                                    cache_strides, num_pages, page, stream)
+
+
+def rtopk_tree_attention(q, q_strides, k_cache, v_cache, cache_strides, dtype, table, table_ld, num_pages, page,
+                         cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale, out, lse, workspace, ws_bytes, stream):
+    return load().rtopk_tree_attention(q, q_strides, k_cache, v_cache, cache_strides, dtype, table, table_ld, num_pages,
+                                       page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale, out, lse, workspace,
+                                       ws_bytes, stream)
+
+
+def rtopk_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page):
+    return load().rtopk_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page)
+
+
+def rtopk_cross_attention(q, q_strides, k, k_strides, v, v_strides, dtype, lens, key_mask, B, N, S, Hq, Hkv, D, scale,
+                          out, lse, workspace, ws_bytes, stream):
+    return load().rtopk_cross_attention(q, q_strides, k, k_strides, v, v_strides, dtype, lens, key_mask, B, N, S, Hq,
+                                        Hkv, D, scale, out, lse, workspace, ws_bytes, stream)
+
+
+def rtopk_cross_attention_workspace_bytes(B, N, S, Hq, Hkv, D):
+    return load().rtopk_cross_attention_workspace_bytes(B, N, S, Hq, Hkv, D)
+
+
 def rtopk_read_probe(src, nbytes, marker, out, stream):
     return load().rtopk_read_probe(src, nbytes, marker, out, stream)
 
@@ -413,6 +461,219 @@ def beam_reorder(src, dst, beam_ids):
     stream = torch.cuda.current_stream(src.device).cuda_stream
     _check(rtopk_beam_reorder(_ptr(src), _ptr(dst), src.shape[0], B, beam, row_bytes, _ptr(beam_ids), ld, stream))
     return dst
+
+
+# ------------------------------------------------------------------ paged cache and attention
+_stride_arrays = {}
+
+
+def _host_strides(st):
+    """A host int64 array of these strides for the C ABI (which reads it during the call)."""
+    arr = _stride_arrays.get(st)
+    if arr is None:
+        if len(_stride_arrays) > 4096:
+            _stride_arrays.clear()
+        arr = _stride_arrays[st] = (ctypes.c_int64 * len(st))(*st)
+    return arr
+
+
+def _strides(t, name):
+    """The strides of all but the last dimension, which has to be contiguous; None where all are."""
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _host_strides(st[:-1])
+
+
+def _ints(t, shape, dev, name):
+    """A contiguous int32 device tensor of this shape."""
+    import torch
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        _on_device(t, dev, name)
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+    return t.data_ptr()
+
+
+def _enqueue(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    import torch
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != RTOPK_OK:
+        raise RtopkError(st, rtopk_last_error())
+
+
+def page_tables(cache_lens, new_lens, page, free_pages, table, num_pages, free_head=None, tokens=None, rows=None,
+                out=None):
+    """Page tables and slot maps from request lengths, on the current stream.
+
+    cache_lens, new_lens [B] int32; free_pages [F] int32; table [B, ld] int32,
+    updated in place; free_head [1] int32 or None. The slots are packed into
+    [tokens], or laid out as [B, rows]; ``out`` may supply the four results.
+    Returns (slots, positions, cu_new [B + 1], free_next [1]), all int32.
+    """
+    import torch
+    dev = table.device
+    if not table.is_cuda or table.dim() != 2:
+        raise ValueError("table must be a [B, ld] device tensor")
+    B, ld = table.shape
+    if out is not None:
+        if len(out) != 4:
+            raise ValueError("out must hold four tensors (slots, positions, cu_new, free_next)")
+        slots, positions, cu, nxt = out
+        shape = slots.shape
+        if slots.dim() not in (1, 2) or (slots.dim() == 2 and shape[0] != B):
+            raise ValueError("out slots must be a [tokens] or [B, rows] tensor")
+        if tokens is not None and shape != (tokens,) or rows is not None and shape != (B, rows):
+            raise ValueError("out slots must have the shape that tokens or rows asks for")
+    else:
+        if (tokens is None) == (rows is None):
+            raise ValueError("give one of tokens (packed slots) and rows (slots per request)")
+        shape = torch.Size((tokens,) if rows is None else (B, rows))
+        slots = torch.empty(shape, dtype=torch.int32, device=dev)
+        positions = torch.empty_like(slots)
+        cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        nxt = torch.empty(1, dtype=torch.int32, device=dev)
+    n = slots.numel()
+    if n == 0 or len(shape) == 2 and shape[1] == 0:
+        raise ValueError("at least one slot is needed")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be a [F] tensor")
+    _enqueue(dev, load().rtopk_page_tables, _ints(cache_lens, (B,), dev, "cache_lens"),
+             _ints(new_lens, (B,), dev, "new_lens"), B, page, _ints(free_pages, free_pages.shape, dev, "free_pages"),
+             free_pages.numel(), None if free_head is None else _ints(free_head, (1,), dev, "free_head"), num_pages,
+             _ints(table, (B, ld), dev, "table"), ld, _ints(slots, shape, dev, "slots"),
+             _ints(positions, shape, dev, "positions"), n, shape[1] if len(shape) == 2 else 0,
+             _ints(cu, (B + 1,), dev, "cu_new"), _ints(nxt, (1,), dev, "free_next"))
+    return slots, positions, cu, nxt
+
+
+def _cache(k_cache, v_cache, dtype, dev):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must be [pages, page, Hkv, D] tensors of the same strides")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise ValueError(f"k_cache and v_cache must be {dtype}")
+    if k_cache.device != dev or v_cache.device != dev:
+        _on_device(k_cache, dev, "k_cache")
+        _on_device(v_cache, dev, "v_cache")
+    return k_cache.shape
+
+
+def cache_store(k, v, slots, k_cache, v_cache):
+    """Stores tokens' keys and values into a paged cache, on the current stream.
+
+    k, v [..., Hkv, D] (the leading dimensions, which must be evenly strided,
+    are the tokens), slots int32 of the leading shape (a slot outside the cache
+    skips its token), k_cache, v_cache [pages, page, Hkv, D]. Returns (k_cache, v_cache).
+    """
+    dev = k.device
+    if not k.is_cuda:
+        raise ValueError("k must be a device tensor")
+    _on_device(v, dev, "v")
+    if k.dim() < 3 or k.shape != v.shape or k.dtype is not v.dtype:
+        raise ValueError("k and v must be [..., Hkv, D] tensors of one shape and type")
+    if slots.shape != k.shape[:-2]:
+        raise ValueError("slots must have the leading shape of k")
+    if k.dim() > 3:
+        k, v = (t.view(-1, *t.shape[-2:]) for t in (k, v))  # raises where the tokens are not evenly strided
+    pages, page, Hkv, D = _cache(k_cache, v_cache, k.dtype, dev)
+    if k.shape[1:] != (Hkv, D):
+        raise ValueError("k and v must have the cache's heads")
+    _enqueue(dev, load().rtopk_cache_store, k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), dtype_code(k),
+             _ints(slots, slots.shape, dev, "slots"), k.shape[0], Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(),
+             _strides(k_cache, "k_cache"), pages, page)
+    return k_cache, v_cache
+
+
+def _attention_args(q, Hkv, scale, out, lse, workspace, dev):
+    """Checks what both attentions share; returns the scale, out and the addresses of lse and the workspace."""
+    import torch
+    B, N, Hq, D = q.shape
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
+        _on_device(out, dev, "out")
+        raise ValueError("out must be a contiguous tensor of q's shape and type")
+    lp = None
+    if lse is not None:
+        if lse.shape != q.shape[:3] or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.device != dev:
+            _on_device(lse, dev, "lse")
+            raise ValueError("lse must be a contiguous float32 [B, N, Hq] tensor")
+        lp = lse.data_ptr()
+    wp, wn = None, 0
+    if workspace is not None:
+        _check_workspace(workspace, dev, 0)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    return scale, out, lp, wp, wn
+
+
+def tree_attention(q, k_cache, v_cache, table, cache_lens, parents=None, sizes=None, scale=None, out=None, lse=None,
+                   workspace=None):
+    """Attention of a tree of drafted tokens over a paged cache, on the current stream.
+
+    q [B, N, Hq, D] float16/bfloat16; k_cache, v_cache [pages, page, Hkv, D];
+    table [B, ld], cache_lens [B], parents [B, N] (None: a chain), sizes [B]
+    (None: N), all int32; scale None = D ** -0.5. ``out`` [B, N, Hq, D] and
+    ``lse`` [B, N, Hq] float32 may be supplied; rows behind a tree's last node
+    keep what they hold. ``workspace`` (zero-filled uint8, of
+    rtopk_tree_attention_workspace_bytes(...) bytes) is needed under graph
+    capture. Returns (out, lse); lse None unless supplied.
+    """
+    dev = q.device
+    if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
+        raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")
+    B, N, Hq, D = q.shape
+    pages, page, Hkv, Dk = _cache(k_cache, v_cache, q.dtype, dev)
+    if Dk != D:
+        raise ValueError("the cache must have q's head size")
+    ld = table.shape[1]
+    scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
+    _enqueue(dev, load().rtopk_tree_attention, q.data_ptr(), _strides(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
+             _strides(k_cache, "k_cache"), dtype_code(q), _ints(table, (B, ld), dev, "table"), ld, pages, page,
+             _ints(cache_lens, (B,), dev, "cache_lens"), None if parents is None else _ints(parents, (B, N), dev, "parents"),
+             None if sizes is None else _ints(sizes, (B,), dev, "sizes"), B, N, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
+    return out, lse
+
+
+def cross_attention(q, k, v, lens=None, key_mask=None, scale=None, out=None, lse=None, workspace=None):
+    """Attention of every beam's rows to its encoder's states, on the current stream.
+
+    q [B, N, Hq, D] (N = beams x tokens) and k, v [B, S, Hkv, D] float16/bfloat16,
+    any strides with a contiguous last dimension; lens [B] int32 (None: S);
+    key_mask [B, S] uint8/bool, nonzero = left out; the rest as
+    tree_attention. Returns (out, lse).
+    """
+    import torch
+    dev = q.device
+    if not q.is_cuda or q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("q must be a [B, N, Hq, D] device tensor and k, v [B, S, Hkv, D]")
+    if k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise ValueError("q, k and v must have one type")
+    if k.device != dev or v.device != dev:
+        _on_device(k, dev, "k")
+        _on_device(v, dev, "v")
+    B, N, Hq, D = q.shape
+    _, S, Hkv, _ = k.shape
+    if k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("k and v must have q's batch and head size")
+    mp = None
+    if key_mask is not None:
+        _on_device(key_mask, dev, "key_mask")
+        if key_mask.shape != (B, S) or key_mask.dtype not in (torch.uint8, torch.bool) or not key_mask.is_contiguous():
+            raise ValueError("key_mask must be a contiguous [B, S] uint8/bool tensor")
+        mp = key_mask.data_ptr()
+    scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
+    _enqueue(dev, load().rtopk_cross_attention, q.data_ptr(), _strides(q, "q"), k.data_ptr(), _strides(k, "k"),
+             v.data_ptr(), _strides(v, "v"), dtype_code(q), None if lens is None else _ints(lens, (B,), dev, "lens"), mp,
+             B, N, S, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
+    return out, lse
 
 
 def debug_step(logits, alive, finished=None, k=None, eos_id=2):

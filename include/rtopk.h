@@ -350,6 +350,139 @@ int rtopk_beam_reorder(const void *src, void *dst, long long nslabs, int B, int 
                        const int32_t *beam_ids, int ld, void *stream);
 
 /*
+ * The decoder layer in front of the selection: a paged key/value cache, the
+ * attention that reads it, and the attention of every beam to its sentence's
+ * encoder states. The LightSeq inference article's decoder is of this shape
+ * (its passages on challenges and on kernel fusion: encoder features,
+ * auto-regressive decoding with a cache); it states no kernel for it.
+ *
+ * A paged cache is two tensors (keys, values) of num_pages pages of `page`
+ * tokens of Hkv heads of D elements. Slot s is token s mod page of page
+ * s / page. Request b's token at position p lies in page table[b][p / page].
+ * Strides are in elements and given as HOST arrays that are read during the
+ * call (NULL = C-contiguous); a stride may be 0 (a broadcast input), not
+ * negative; the D elements of a head are contiguous.
+ */
+
+/*
+ * Page tables and slot maps from request lengths. Request b holds
+ * c = cache_lens[b] tokens and takes n = new_lens[b] more (negative counts as
+ * 0). It keeps the first ceil(c / page) entries of its table row and takes
+ * the ceil((c + n) / page) - ceil(c / page) pages it lacks from the free list,
+ * in order of requests: its first one is free_pages[free_head + (pages that
+ * requests 0 .. b-1 need)]. Its new token t gets the slot
+ *     table[b][(c + t) / page] * page + (c + t) mod page
+ * and the position c + t.
+ *   cache_lens, new_lens   device [B] int32
+ *   free_pages  device [nfree] int32, ids of unused pages (may be NULL when nfree is 0)
+ *   free_head   device [1] int32, place of the list's first unused id; NULL = 0
+ *   table       device [B][table_ld] int32, updated in place: only entries of
+ *               newly taken pages are written
+ *   slots       device [T] int32; positions device [T] int32 or NULL. rows = 0:
+ *               packed, request b's tokens at cu_new[b] ..; rows > 0: T = B*rows,
+ *               request b's tokens at b*rows ... Entries without a token are -1.
+ *   cu_new      device [B+1] int32: sums of the new lengths before each request
+ *               (held at 2^31-1 past it)
+ *   free_next   device [1] int32 or NULL, not free_head: free_head plus the pages taken
+ * A request is refused when its tokens exceed its table row (table_ld*page),
+ * its row of slots (rows) or the T packed slots, or when the list is too short
+ * for it: it takes no page, its tokens' slots and positions are -1, its table
+ * row stays. A request refused for its table row or row of slots counts no
+ * pages towards those after it; one refused for a short list or the T slots
+ * does, so that every later request that needs pages is refused too. A page
+ * id outside [0, num_pages) gives slot -1.
+ * B <= 65536; num_pages*page and table_ld*page < 2^31. Asynchronous on
+ * `stream`; one launch, no workspace.
+ */
+int rtopk_page_tables(const int32_t *cache_lens, const int32_t *new_lens, int B, int page,
+                      const int32_t *free_pages, int nfree, const int32_t *free_head, int num_pages, int32_t *table,
+                      int table_ld, int32_t *slots, int32_t *positions, int T, int rows, int32_t *cu_new,
+                      int32_t *free_next, void *stream);
+
+/*
+ * Stores T tokens' keys and values into the cache: k[t], v[t] go to slot
+ * slots[t]; a slot outside [0, num_pages*page) (the -1 of padding) skips the
+ * token, and everything else in the cache stays as it was. Slots of one call
+ * must be distinct (those of rtopk_page_tables are, when the free list and
+ * the table rows name distinct pages): where two tokens name one slot, each
+ * 16 bytes of it come from an unspecified one of them.
+ *   k, v       device [T][Hkv][D]; k_strides, v_strides HOST [2] (token, head)
+ *   k_cache, v_cache  device [num_pages][page][Hkv][D], not overlapping k or v;
+ *              cache_strides HOST [3] (page, token, head), the same for both
+ *   dtype      any of the three; D >= 1. Rows move as 16-byte vectors when all
+ *              pointers and strides and D*size are multiples of 16 bytes, else
+ *              element by element
+ * Hkv*D <= 2^20. Asynchronous on `stream`; one launch, no workspace.
+ */
+int rtopk_cache_store(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides, int dtype,
+                      const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache,
+                      const int64_t *cache_strides, int num_pages, int page, void *stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache. Request b holds
+ * L = cache_lens[b] tokens, followed at positions L, L+1, ... by the tokens of
+ * its tree's nodes (rtopk_cache_store puts them there). Node i sees the L
+ * tokens before the tree, its ancestors and itself:
+ *     x_ij = scale * (q_i . k_j),  out_i = sum_j exp(x_ij - lse_i) v_j,
+ *     lse_i = log(sum_j exp(x_ij)),
+ * per query head; query head h reads key head h / (Hq / Hkv). The parents of a
+ * level are the beam ids that rtopk_beam_step returns for it, shifted to the
+ * nodes of the level before; a tree of one node is the decode step of a single
+ * token, a chain (parents NULL) that of N causal tokens.
+ *   q          device [B][N][Hq][D] float16 or bfloat16 (float32: RTOPK_ENOTSUP);
+ *              q_strides HOST [3] (batch, node, head)
+ *   k_cache, v_cache  device [num_pages][page][Hkv][D], same type; cache_strides
+ *              HOST [3] (page, token, head), the same for both
+ *   table      device [B][table_ld] int32
+ *   cache_lens device [B] int32, held to [0, table_ld*page]
+ *   parents    device [B][N] int32, parents[b][i] in [0, i) or no parent (any
+ *              other value); NULL = i - 1
+ *   sizes      device [B] int32, nodes of each tree, held to [0, N]; NULL = N.
+ *              Rows i >= sizes[b] of out and lse stay as they were
+ *   out        device [B][N][Hq][D], contiguous, type of q, 16-byte aligned
+ *   lse        device [B][N][Hq] float32 or NULL (natural logarithm)
+ * Tokens past the table row (position >= table_ld*page) or on a page outside
+ * [0, num_pages) are left out and never read. A key that a row may not see does not
+ * touch it, whatever its key and value hold (infinities and NaN included). A
+ * row that sees no key (or none with x > -inf) gives out = 0 and lse = -inf.
+ * Scores, sums and outputs are accumulated in float32, weights rounded to the
+ * type of q for the product with the values. The same call gives the same
+ * bits. N <= 256, D a multiple of 8 up to 256, Hkv divides Hq, pointers
+ * 16-byte aligned (int32 and float arrays 4-byte), strides multiples of 8.
+ * Workspace: as rtopk_cross_attention.
+ */
+int rtopk_tree_attention(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
+                         const int64_t *cache_strides, int dtype, const int32_t *table, int table_ld, int num_pages,
+                         int page, const int32_t *cache_lens, const int32_t *parents, const int32_t *sizes, int B,
+                         int N, int Hq, int Hkv, int D, float scale, void *out, float *lse, void *workspace,
+                         size_t ws_bytes, void *stream);
+size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int table_ld, int page);
+
+/*
+ * Cross attention of N query rows per batch element (beams x tokens) to the
+ * S states of its encoder, which all its beams share. As rtopk_tree_attention
+ * with every row seeing the same keys: j < lens[b], and key_mask[b][j] == 0.
+ *   q          device [B][N][Hq][D]; q_strides HOST [3] (batch, row, head)
+ *   k, v       device [B][S][Hkv][D]; k_strides, v_strides HOST [3] (batch, token, head)
+ *   lens       device [B] int32, held to [0, S]; NULL = S
+ *   key_mask   device [B][S] uint8, nonzero = left out; NULL = none
+ *   out, lse   as rtopk_tree_attention (N any, B*N*Hq*D < 2^31)
+ * Workspace: keys are split over workgroups when there are few rows, and the
+ * parts are joined in a fixed order. workspace NULL uses the library-owned
+ * workspace of `stream` (as rtopk_beam_step); a call that a graph captures is
+ * then refused (RTOPK_EINVAL) if it needs one. A caller's workspace holds
+ * ws_bytes >= rtopk_cross_attention_workspace_bytes(...) bytes, 256-byte
+ * aligned, zero-filled before its first use (it may be one of
+ * rtopk_beam_step_ws); calls sharing it must be ordered, so graphs that may
+ * run at the same time need one each.
+ */
+int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                          const void *v, const int64_t *v_strides, int dtype, const int32_t *lens,
+                          const uint8_t *key_mask, int B, int N, int S, int Hq, int Hkv, int D, float scale, void *out,
+                          float *lse, void *workspace, size_t ws_bytes, void *stream);
+size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hkv, int D);
+
+/*
  * Measurement aid, not part of the selection: a plain streaming read that
  * gives the practical HBM ceiling the selection kernel is compared with. It
  * reads `bytes` bytes at `src` once with 16-byte non-temporal loads (ten per
