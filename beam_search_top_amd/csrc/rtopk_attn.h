@@ -60,8 +60,21 @@ struct AttnArgs {
     const int32_t *sizes;      // tree: [B] nodes, or null (N)
     void *out;                 // [B][N][Hq][D]
     float *lse;                // [B][N][Hq] or null
+    // the split over workgroups (plan_attention)
+    int row_tiles, nsplit, min_tiles;
+    float *part;               // [B][Hkv][nsplit][N * G][dp] unnormalised outputs of the splits
+    float *ml;                 // [B][Hkv][nsplit][N * G][2] their maxima (base 2) and sums
 };
-hipError_t launch_attention(const AttnArgs &a, int dtype, bool tree, hipStream_t s);
+
+// How a call is cut: workgroups of `waves` x 32 rows, tiles of `bn` keys,
+// heads padded to `dp` elements, keys in at most `nsplit` parts.
+struct AttnPlan {
+    int dp, bn, waves, row_tiles, nsplit, min_tiles;
+    int64_t grid;
+    size_t ml_off, part_off, ws_bytes; // workspace behind the fixed region
+};
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S);
+hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s);
 
 // Calls `launch` with a library-owned workspace of `need` bytes for `stream`
 // (rtopk_host.cpp), held until it returns; a status code.

@@ -9,133 +9,568 @@
 
 #include "rtopk_attn.h"
 
+#include <type_traits>
+
 namespace rtopk {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void glb_void;
+
+// The 16-bit types: 1 float16, 2 bfloat16.
 template <int DT> struct Elem;
 template <> struct Elem<1> {
     typedef _Float16 T;
+    static constexpr uint32_t kExp = 0x7c00u; // exponent bits: all set in infinities and NaN
+    typedef T V8 __attribute__((ext_vector_type(8)));
+    typedef T V2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
 };
 template <> struct Elem<2> {
     typedef __bf16 T;
+    static constexpr uint32_t kExp = 0x7f80u;
+    typedef T V8 __attribute__((ext_vector_type(8)));
+    typedef T V2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
 };
 
-// One wave per query row and head: the lanes share the keys for the scores and
-// the head's elements for the outputs.
-template <int DT, bool TREE> __global__ __launch_bounds__(64) void attn_rows(const AttnArgs a)
+// The keys of a row that counts no key come from here.
+__device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
+
+// Workgroup w runs on XCD w mod 8; logical workgroup numbers give every XCD
+// one contiguous part of the grid, so that workgroups that read the same keys
+// share an L2.
+__device__ __forceinline__ int xcd_order(int w, int n)
+{
+    const int per = n / 8, rest = n % 8, x = w % 8;
+    return x * per + (x < rest ? x : rest) + w / 8;
+}
+
+// Keys of batch element b that any of its rows may see: [0, end), and where its
+// tree begins (tree: the nodes are at tree0 ... tree0 + size - 1).
+struct KeyRange {
+    int end, tree0, size;
+};
+
+template <bool TREE> __device__ __forceinline__ KeyRange key_range(const AttnArgs &a, int b)
+{
+    KeyRange r;
+    if (TREE) {
+        const int sz = a.sizes ? a.sizes[b] : a.N, L = a.lens[b];
+        r.size = sz < 0 ? 0 : sz > a.N ? a.N : sz;
+        r.tree0 = L < 0 ? 0 : L > a.S ? a.S : L;
+        r.end = r.tree0 + r.size < a.S ? r.tree0 + r.size : a.S;
+    } else {
+        const int L = a.lens ? a.lens[b] : a.S;
+        r.size = a.N;
+        r.end = r.tree0 = L < 0 ? 0 : L > a.S ? a.S : L;
+    }
+    return r;
+}
+
+// A batch element's keys are tiles of `bn`; split s takes tiles [s * per, ...).
+__device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
+{
+    const int per = (tiles + a.nsplit - 1) / a.nsplit;
+    return per > a.min_tiles ? per : a.min_tiles;
+}
+
+// The tile kernel. A workgroup of WR waves takes 32 * WR query rows of one key
+// head (rows = nodes or beams x the query heads of the group, which all read
+// the same keys) and walks over a range of keys, BN at a time.
+//
+// Scores are computed transposed, X^T = K Q^T, by v_mfma_f32_32x32x16: a lane
+// then holds 16 keys of one query row per 32 x 32 block (row l mod 32, keys
+// 8 (i / 4) + 4 (l / 32) + i mod 4), so that maxima and sums over keys stay in
+// the lane and end in one exchange between the lane halves, and the weights
+// are already the B operand of O^T = V^T P^T: a contraction may go over the
+// keys in any order, and lane l's eight keys of step c are registers 8c ... 8c+7.
+// The A operand V^T, four keys of one column per load, comes from the
+// row-major tile by transposing LDS reads.
+//
+// Keys and values come by direct-to-LDS loads, double-buffered: while a tile is
+// multiplied, the next one is in flight. A row of a tile is DP elements; its
+// 16-byte chunks are permuted by the row (slot = chunk ^ f(row)), which keeps
+// both kinds of reads free of bank conflicts. A key that no row may see (past
+// the end, masked out, on a page that does not exist) is loaded from a line of
+// zeros: 0 * infinity would spread to every row.
+//
+// The running maximum m of a row moves only when a tile exceeds it by more
+// than 2^8 (weights then stay below 2^8, which costs no precision), which makes
+// the rescaling of the accumulators rare. Weights are rounded to the inputs'
+// type, because the matrix instructions take nothing else next to it: half a
+// step per weight, as much as the output's own rounding. Their sum is of the
+// unrounded ones, in float32.
+constexpr float kLazy = 8.f;
+
+template <int DT, int DP, int WR, bool TREE> __global__ __launch_bounds__(64 * WR) void attn_tiles(const AttnArgs a)
+{
+    typedef Elem<DT> E;
+    typedef typename E::T T;
+    typedef typename E::V8 V8;
+    typedef typename E::V2 V2;
+    constexpr int BN = DP > 128 ? 32 : 64; // keys per tile
+    constexpr int KB = BN / 32, DB = DP / 32, DC = DP / 16, CH = DP / 8;
+    constexpr int ROWB = DP * 2, TILEB = BN * ROWB;   // bytes of a row and of a tile
+    constexpr int RPL = 1024 / ROWB;                  // rows of one 1 KiB load of a wave
+    constexpr int NI = BN / RPL / WR > 0 ? BN / RPL / WR : 1; // loads per wave and tensor
+    static_assert(BN % (RPL * WR) == 0, "a tile is whole loads of every wave");
+    constexpr int FK = CH < 16 ? CH - 1 : 15;
+    constexpr int kWords = kMaxTree / 64;
+    __shared__ __align__(1024) uint8_t smem[4 * TILEB]; // K tiles 0 and 1, V tiles 0 and 1
+    __shared__ uint64_t s_up[TREE ? kMaxTree * kWords : 1]; // ancestors of every node
+    __shared__ int s_jump[TREE ? kMaxTree : 1];
+    __shared__ uint64_t s_odd[2]; // keys of the tile with infinities or NaN in their values
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    int w = xcd_order((int)blockIdx.x, (int)gridDim.x);
+    const int rt = w % a.row_tiles;
+    w /= a.row_tiles;
+    const int split = w % a.nsplit;
+    w /= a.nsplit;
+    const int hk = w % a.Hkv, b = w / a.Hkv;
+
+    const KeyRange kr = key_range<TREE>(a, b);
+    const int R = kr.size * a.G, r0 = rt * 32 * WR;
+    if (r0 >= R)
+        return;
+    const int tiles = (kr.end + BN - 1) / BN, per = tiles_per_split(tiles, a);
+    const int t_begin = split * per;
+    if (split > 0 && t_begin >= tiles)
+        return;
+    const int t_end = t_begin + per < tiles ? t_begin + per : tiles;
+    const bool whole = per >= tiles; // the only split: it writes the outputs itself
+
+    // this lane's query row
+    const int row = r0 + wave * 32 + col;
+    const bool live = row < R;
+    const int node = live ? row / a.G : 0, head = hk * a.G + (live ? row - node * a.G : 0);
+    V8 q[DC];
+    {
+        const T *qp = static_cast<const T *>(a.q) + b * a.qs[0] + node * a.qs[1] + head * a.qs[2];
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u; // scores by |scale|: the maximum stays a maximum
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+            const int d = 16 * c + 8 * half;
+            u32x4 x = {0, 0, 0, 0};
+            if (live && d < a.D)
+                x = *reinterpret_cast<const u32x4 *>(qp + d);
+            x ^= flip;
+            q[c] = __builtin_bit_cast(V8, x);
+        }
+    }
+    const float cs = fabsf(a.scale) * kLog2e;
+
+    // ---- ancestors, by pointer doubling: after round r, s_up[i] holds the
+    // nearest 2^r nodes above i (i among them) and s_jump[i] the next one
+    const bool walk = TREE && kr.size > 1 && t_end * BN > kr.tree0; // this split meets the tree
+    if (TREE && walk && a.parents) {
+        constexpr int PER = (kMaxTree + 64 * WR - 1) / (64 * WR);
+#pragma unroll
+        for (int q0 = 0; q0 < PER; ++q0) {
+            const int i = tid + q0 * 64 * WR;
+            if (i < kr.size) {
+                s_jump[i] = parent_of(a.parents[(int64_t)b * a.N + i], i);
+#pragma unroll
+                for (int x = 0; x < kWords; ++x)
+                    s_up[i * kWords + x] = (i >> 6) == x ? 1ull << (i & 63) : 0;
+            }
+        }
+        __syncthreads();
+        for (int span = 1; span < kr.size; span <<= 1) {
+            uint64_t up[PER][kWords];
+            int jump[PER];
+#pragma unroll
+            for (int q0 = 0; q0 < PER; ++q0) {
+                const int i = tid + q0 * 64 * WR;
+                jump[q0] = -1;
+                const int j = i < kr.size ? s_jump[i] : -1;
+                if (j >= 0) {
+                    jump[q0] = s_jump[j];
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x)
+                        up[q0][x] = s_up[i * kWords + x] | s_up[j * kWords + x];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int q0 = 0; q0 < PER; ++q0) {
+                const int i = tid + q0 * 64 * WR;
+                if (i < kr.size && s_jump[i] >= 0) {
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x)
+                        s_up[i * kWords + x] = up[q0][x];
+                    s_jump[i] = jump[q0];
+                }
+            }
+            __syncthreads();
+        }
+    }
+    // whether this row's node sees key j of the tile at t0, one bit per key
+    auto window = [&](int t0) -> uint64_t {
+        const int off = t0 - kr.tree0; // node of the tile's first key
+        auto word = [&](int x) -> uint64_t {
+            if (x < 0 || x >= kWords || node >= kr.size)
+                return 0;
+            if (a.parents)
+                return s_up[node * kWords + x];
+            const int n = node - 64 * x + 1; // a chain: nodes 0 ... node
+            return n >= 64 ? ~0ull : n > 0 ? (1ull << n) - 1 : 0;
+        };
+        if (off <= -64)
+            return ~0ull;
+        if (off < 0)
+            return (word(0) << -off) | ((1ull << -off) - 1);
+        const int x = off >> 6, sh = off & 63;
+        return sh ? (word(x) >> sh) | (word(x + 1) << (64 - sh)) : word(x);
+    };
+
+    // ---- loads. Lane l of a wave's load i brings slot l mod CH of row
+    // (wave * NI + i) * RPL + l / CH
+    const char *kbase = static_cast<const char *>(a.k) + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
+    const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
+    const int lrow = lane / CH, lslot = lane % CH;
+    auto fv = [](int r) { return CH < 16 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; };
+    // what decides about key t0 + lane, read one tile ahead: its page, or its mask
+    auto fetch = [&](int t) -> int {
+        const int j = t * BN + lane;
+        if (lane >= BN || j >= kr.end)
+            return -1;
+        if (TREE)
+            return a.table[(int64_t)b * a.ld + page_of(a.page, (uint32_t)j)];
+        return a.key_mask ? a.key_mask[(int64_t)b * a.S + j] : 0;
+    };
+    // starts the loads of tile t into buffer `buf`; the keys that count, one bit each
+    auto issue = [&](int t, int buf, int info) -> uint64_t {
+        const int j = t * BN + lane;
+        bool ok = lane < BN && j < kr.end;
+        int64_t off = 0;
+        if (TREE) {
+            const int id = checked_page(info, a.num_pages);
+            ok = ok && id >= 0;
+            const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : 0));
+            off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
+        } else {
+            ok = ok && info == 0;
+        }
+        const uint64_t oks = __ballot(ok);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int lr = (wave * NI + i) * RPL, r = lr + lrow;
+            const int ck = lslot ^ (r & FK), cv = lslot ^ fv(r);
+            const char *kp, *vp;
+            bool in;
+            if (TREE) {
+                const int64_t o = ((int64_t)__shfl((int)(off >> 32), r) << 32) | (uint32_t)__shfl((int)off, r);
+                in = o >= 0;
+                kp = kbase + o;
+                vp = vbase + o;
+            } else {
+                in = oks >> r & 1;
+                kp = kbase + 2 * (int64_t)(t * BN + r) * a.ks[1];
+                vp = vbase + 2 * (int64_t)(t * BN + r) * a.vs[1];
+            }
+            const char *z = reinterpret_cast<const char *>(g_zeros);
+            kp = in && ck * 8 < a.D ? kp + ck * 16 : z;
+            vp = in && cv * 8 < a.D ? vp + cv * 16 : z;
+            __builtin_amdgcn_global_load_lds((glb_void *)kp, (lds_void *)(smem + buf * TILEB + lr * ROWB), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((glb_void *)vp, (lds_void *)(smem + (2 + buf) * TILEB + lr * ROWB), 16, 0, 0);
+        }
+        return oks;
+    };
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+        o[d] = f32x16{};
+    float m = -INFINITY, l = 0.f;
+
+    // this lane's operand addresses: K row `col`, and the V rows of its 16-lane group
+    const int kaddr = col * ROWB;
+    const int vrow = 4 * half + ((lane & 15) >> 2), vchunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    int vaddr[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+        vaddr[d] = vrow * ROWB + ((4 * d + vchunk) ^ fv(vrow)) * 16 + (lane & 1) * 8;
+
+    uint64_t oks = 0;
+    int info = 0;
+    if (t_begin < t_end) {
+        oks = issue(t_begin, 0, fetch(t_begin));
+        info = fetch(t_begin + 1);
+    }
+    for (int t = t_begin; t < t_end; ++t) {
+        const int buf = (t - t_begin) & 1;
+        // tile t is in LDS; every wave is done with the other buffer
+        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt(0)
+        __syncthreads();
+        const uint64_t now = oks;
+        if (t + 1 < t_end) {
+            oks = issue(t + 1, buf ^ 1, info);
+            info = fetch(t + 2);
+        }
+        const uint8_t *ks = smem + buf * TILEB, *vs = smem + (2 + buf) * TILEB;
+
+        // ---- scores
+        f32x16 x[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            x[k] = f32x16{};
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+                const V8 kf = *reinterpret_cast<const V8 *>(ks + k * 32 * ROWB + kaddr + ((2 * c + half) ^ (col & FK)) * 16);
+                x[k] = E::mfma(kf, q[c], x[k]);
+            }
+        }
+        const bool in_tree = walk && (t + 1) * BN > kr.tree0;
+        const uint64_t all = BN == 64 ? ~0ull : (1ull << BN) - 1;
+        uint64_t see = now;
+        const bool masked = now != all || in_tree;
+        if (masked) {
+            if (in_tree)
+                see &= window(t * BN);
+            const uint64_t bits = see >> (4 * half);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : -INFINITY;
+        }
+        // ---- the running maximum
+        float mx = x[0][0];
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                mx = fmaxf(mx, x[k][i]);
+        {
+            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+            mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+        }
+        mx *= cs;
+        if (__any(mx > m + kLazy)) {
+            const float mn = mx > m ? mx : m;
+            const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn); // from -inf: 0
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                o[d] *= f;
+        }
+        // ---- weights
+        const float mu = m == -INFINITY ? 0.f : m;
+        V8 p[KB][2];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][i], cs, -mu));
+        }
+        if (masked && cs == 0.f) { // 0 * -inf is not -inf
+            const uint64_t bits = see >> (4 * half);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                l += x[k][i];
+                p[k][i / 8][i % 8] = (T)x[k][i];
+            }
+        // ---- a node's infinities and NaN must not reach the rows that do not
+        // see it: they leave the tile, and are added afterwards where they belong
+        uint64_t odd = 0;
+        if (TREE && in_tree) {
+            if (tid < 2)
+                s_odd[tid] = 0;
+            __syncthreads();
+            uint8_t *vw = smem + (2 + buf) * TILEB;
+            for (int u = tid; u < TILEB / 16; u += 64 * WR) {
+                u32x4 *at = reinterpret_cast<u32x4 *>(vw + u * 16);
+                u32x4 y = *at;
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool lo = (y[e] & E::kExp) == E::kExp, hi = (y[e] >> 16 & E::kExp) == E::kExp;
+                    any = any || lo || hi;
+                    y[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                }
+                if (any) {
+                    *at = y;
+                    atomicOr((unsigned long long *)&s_odd[0], 1ull << (u / CH));
+                }
+            }
+            __syncthreads();
+            odd = s_odd[0];
+        }
+        // ---- outputs
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint8_t *vp = vs + vaddr[d] + (32 * k + 16 * c) * ROWB;
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)vp);
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vp + 8 * ROWB));
+                    const V8 vf = __builtin_bit_cast(V8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                    o[d] = E::mfma(vf, p[k][c], o[d]);
+                }
+        while (TREE && odd) {
+            const int j = __ffsll((unsigned long long)odd) - 1;
+            odd &= odd - 1;
+            if (!(see >> j & 1))
+                continue;
+            const int pos = t * BN + j, pg = (int)page_of(a.page, (uint32_t)pos);
+            const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
+            const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                    if (e < a.D) {
+                        const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
+                        if ((raw & E::kExp) == E::kExp)
+                            o[d][i] += (float)vr[e];
+                    }
+                }
+        }
+    }
+    {
+        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+        l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
+    }
+    if (!live)
+        return;
+    if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = ((int64_t)b * a.N + node) * a.Hq + head;
+        T *out = static_cast<T *>(a.out) + at * a.D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int e = 32 * d + 8 * g + 4 * half;
+                if (e < a.D) {
+                    T y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = (T)(l == 0.f ? 0.f : o[d][4 * g + i] * inv);
+                    *reinterpret_cast<uint64_t *>(out + e) = __builtin_bit_cast(uint64_t, y);
+                }
+            }
+        if (a.lse && half == 0)
+            a.lse[at] = l == 0.f ? -INFINITY : (m + __builtin_log2f(l)) * kLn2;
+    } else {
+        const int64_t at = ((((int64_t)b * a.Hkv + hk) * a.nsplit + split) * a.N * a.G + row);
+        float *po = a.part + at * DP;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
+                    f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+        if (half == 0) {
+            a.ml[2 * at] = m;
+            a.ml[2 * at + 1] = l;
+        }
+    }
+}
+
+// Joins the splits of a row in their order: a wave per row, four consecutive
+// elements per lane at a time.
+template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int bn)
 {
     typedef typename Elem<DT>::T T;
-    __shared__ float sq[kMaxHeadDim], sp[64];
-    __shared__ int64_t sv[64];
-    const int lane = threadIdx.x;
-    const int h = blockIdx.x % a.Hq, n = (blockIdx.x / a.Hq) % a.N, b = blockIdx.x / a.Hq / a.N;
-    const int hk = h / a.G;
-    int L = a.S, tree0 = 0x7fffffff;
-    uint64_t up[kMaxTree / 64] = {};
-    if (TREE) {
-        int sz = a.sizes ? a.sizes[b] : a.N;
-        sz = sz < 0 ? 0 : sz > a.N ? a.N : sz;
-        if (n >= sz)
-            return;
-        L = a.lens[b];
-        L = L < 0 ? 0 : L > a.S ? a.S : L;
-        tree0 = L;
-        L = L + sz < a.S ? L + sz : a.S;
-        for (int i = n; i >= 0; i = a.parents ? parent_of(a.parents[(int64_t)b * a.N + i], i) : i - 1)
-            for (int w = 0; w < kMaxTree / 64; ++w)
-                up[w] |= (i >> 6) == w ? 1ull << (i & 63) : 0;
-    } else if (a.lens) {
-        L = a.lens[b];
-        L = L < 0 ? 0 : L > a.S ? a.S : L;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (id >= (int64_t)a.B * a.Hkv * a.N * a.G)
+        return;
+    const int row = (int)(id % (a.N * a.G));
+    const int hk = (int)(id / (a.N * a.G) % a.Hkv), b = (int)(id / (a.N * a.G) / a.Hkv);
+    const KeyRange kr = key_range<TREE>(a, b);
+    const int tiles = (kr.end + bn - 1) / bn, per = tiles_per_split(tiles, a);
+    if (row >= kr.size * a.G || per >= tiles)
+        return;
+    const int n = (tiles + per - 1) / per; // splits with keys
+    const int64_t at0 = ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G + row, step = (int64_t)a.N * a.G;
+    float M = -INFINITY, L = 0.f;
+    for (int s = 0; s < n; ++s)
+        M = fmaxf(M, a.ml[2 * (at0 + s * step)]);
+    const float mu = M == -INFINITY ? 0.f : M;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n; ++s) {
+        const float f = __builtin_amdgcn_exp2f(a.ml[2 * (at0 + s * step)] - mu);
+        L += f * a.ml[2 * (at0 + s * step) + 1];
+        if (4 * lane < DP)
+            acc += f * *reinterpret_cast<const f32x4 *>(a.part + (at0 + s * step) * DP + 4 * lane);
     }
-    const T *q = static_cast<const T *>(a.q) + b * a.qs[0] + n * a.qs[1] + h * a.qs[2];
-    for (int d = lane; d < a.D; d += 64)
-        sq[d] = (float)q[d];
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, o[kMaxHeadDim / 64] = {};
-    for (int j0 = 0; j0 < L; j0 += 64) {
-        const int j = j0 + lane;
-        bool ok = j < L;
-        int64_t ko = 0, vo = 0;
-        if (TREE) {
-            if (ok && j >= tree0) {
-                const int t = j - tree0;
-                bool in = false;
-                for (int w = 0; w < kMaxTree / 64; ++w)
-                    in |= (t >> 6) == w && (up[w] >> (t & 63) & 1);
-                ok = in;
-            }
-            if (ok) {
-                const int pg = (int)page_of(a.page, (uint32_t)j);
-                const int id = checked_page(a.table[(int64_t)b * a.ld + pg], a.num_pages);
-                ok = id >= 0;
-                ko = vo = id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1] + hk * a.ks[2];
-            }
-        } else {
-            if (ok && a.key_mask)
-                ok = a.key_mask[(int64_t)b * a.S + j] == 0;
-            ko = b * a.ks[0] + j * a.ks[1] + hk * a.ks[2];
-            vo = b * a.vs[0] + j * a.vs[1] + hk * a.vs[2];
-        }
-        float x = -INFINITY;
-        if (ok) {
-            const T *k = static_cast<const T *>(a.k) + ko;
-            float s = 0.f;
-            for (int d = 0; d < a.D; ++d)
-                s += sq[d] * (float)k[d];
-            x = s * (a.scale * kLog2e);
-        }
-        float mt = x;
-        for (int w = 1; w < 64; w <<= 1)
-            mt = fmaxf(mt, __shfl_xor(mt, w));
-        const float mn = fmaxf(m, mt);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float p = ok && x != -INFINITY ? exp2f(x - mn) : 0.f;
-        m = mn;
-        float ps = p;
-        for (int w = 1; w < 64; w <<= 1)
-            ps += __shfl_xor(ps, w);
-        l = l * f + ps;
-        __syncthreads();
-        sp[lane] = p;
-        sv[lane] = ok ? vo : -1;
-        __syncthreads();
-        for (int c = 0; c < kMaxHeadDim / 64; ++c) {
-            const int d = c * 64 + lane;
-            float acc = o[c] * f;
-            if (d < a.D)
-                for (int i = 0; i < 64; ++i)
-                    if (sv[i] >= 0)
-                        acc += sp[i] * (float)(static_cast<const T *>(a.v) + sv[i])[d];
-            o[c] = acc;
-        }
-    }
-    T *out = static_cast<T *>(a.out) + (((int64_t)b * a.N + n) * a.Hq + h) * a.D;
-    for (int c = 0; c < kMaxHeadDim / 64; ++c) {
-        const int d = c * 64 + lane;
-        if (d < a.D)
-            out[d] = (T)(l == 0.f ? 0.f : o[c] / l);
+    const int node = row / a.G, head = hk * a.G + row - node * a.G;
+    const int64_t at = ((int64_t)b * a.N + node) * a.Hq + head;
+    if (4 * lane < a.D) {
+        T y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = (T)(L == 0.f ? 0.f : acc[i] / L);
+        *reinterpret_cast<uint64_t *>(static_cast<T *>(a.out) + at * a.D + 4 * lane) = __builtin_bit_cast(uint64_t, y);
     }
     if (a.lse && lane == 0)
-        a.lse[((int64_t)b * a.N + n) * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_log2f(L)) * kLn2;
+}
+
+template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+{
+    const dim3 grid((unsigned)p.grid);
+    if (p.waves == 1)
+        hipLaunchKernelGGL((attn_tiles<DT, DP, 1, TREE>), grid, dim3(64), 0, s, a);
+    else if (p.waves == 2)
+        hipLaunchKernelGGL((attn_tiles<DT, DP, 2, TREE>), grid, dim3(128), 0, s, a);
+    else
+        hipLaunchKernelGGL((attn_tiles<DT, DP, 4, TREE>), grid, dim3(256), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.nsplit > 1) {
+        const int64_t rows = (int64_t)a.B * a.N * a.Hq;
+        hipLaunchKernelGGL((attn_join<DT, DP, TREE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a, p.bn);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <int DT, bool TREE> hipError_t launch_type(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+{
+    if (p.dp == 64)
+        return launch_dims<DT, 64, TREE>(a, p, s);
+    if (p.dp == 128)
+        return launch_dims<DT, 128, TREE>(a, p, s);
+    return launch_dims<DT, 256, TREE>(a, p, s);
 }
 
 } // namespace
 
-hipError_t launch_attention(const AttnArgs &a, int dtype, bool tree, hipStream_t s)
+hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)a.B * a.N * a.Hq)), block(64);
-    if (dtype == 1 && tree)
-        hipLaunchKernelGGL((attn_rows<1, true>), grid, block, 0, s, a);
-    else if (dtype == 1)
-        hipLaunchKernelGGL((attn_rows<1, false>), grid, block, 0, s, a);
-    else if (tree)
-        hipLaunchKernelGGL((attn_rows<2, true>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((attn_rows<2, false>), grid, block, 0, s, a);
-    return hipGetLastError();
+    if (dtype == 1)
+        return tree ? launch_type<1, true>(a, p, s) : launch_type<1, false>(a, p, s);
+    return tree ? launch_type<2, true>(a, p, s) : launch_type<2, false>(a, p, s);
 }
 
 } // namespace rtopk

@@ -85,21 +85,61 @@ int check_attention(const char *what, int dtype, int B, int N, int Hq, int Hkv, 
     return RTOPK_OK;
 }
 
-int enqueue_attention(const char *what, const rtopk::AttnArgs &a, int dtype, bool tree, void *workspace, size_t ws_bytes,
+int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree, void *workspace, size_t ws_bytes,
                       hipStream_t stream)
 {
-    const size_t need = rtopk::kWsFixedBytes;
+    const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S);
     if (workspace && (uintptr_t)workspace % 256)
         return set_error(RTOPK_EINVAL, "%s: workspace is not 256-byte aligned", what);
-    if (workspace && ws_bytes < need)
-        return set_error(RTOPK_ENOMEM, "%s: workspace of %zu bytes is smaller than the %zu needed", what, ws_bytes, need);
-    const hipError_t e = rtopk::launch_attention(a, dtype, tree, stream);
-    if (e != hipSuccess)
-        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
-    return RTOPK_OK;
+    if (workspace && ws_bytes < p.ws_bytes)
+        return set_error(RTOPK_ENOMEM, "%s: workspace of %zu bytes is smaller than the %zu needed", what, ws_bytes,
+                         p.ws_bytes);
+    if (p.grid > INT_MAX)
+        return set_error(RTOPK_ENOTSUP, "%s: %lld workgroups exceed one launch", what, (long long)p.grid);
+    a.row_tiles = p.row_tiles;
+    a.nsplit = p.nsplit;
+    a.min_tiles = p.min_tiles;
+    const auto go = [&](void *ws) {
+        a.ml = ws ? (float *)((uint8_t *)ws + p.ml_off) : nullptr;
+        a.part = ws ? (float *)((uint8_t *)ws + p.part_off) : nullptr;
+        const hipError_t e = rtopk::launch_attention(a, p, dtype, tree, stream);
+        if (e != hipSuccess)
+            return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+        return (int)RTOPK_OK;
+    };
+    if (p.nsplit == 1 || workspace)
+        return go(p.nsplit == 1 ? nullptr : workspace);
+    return rtopk::with_workspace(p.ws_bytes, stream, go);
 }
 
 } // namespace
+
+namespace rtopk {
+
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S)
+{
+    AttnPlan p{};
+    p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    p.bn = p.dp > 128 ? 32 : 64;
+    const int64_t R = (int64_t)N * (Hq / Hkv);
+    p.waves = R <= 32 ? 1 : R <= 64 ? 2 : 4;
+    p.row_tiles = (int)((R + 32 * p.waves - 1) / (32 * p.waves));
+    const int64_t groups = (int64_t)B * Hkv * p.row_tiles, tiles = ((int64_t)S + p.bn - 1) / p.bn;
+    p.min_tiles = 4;
+    int64_t want = (512 + groups - 1) / groups; // two workgroups per CU
+    const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
+    want = want < most ? want : most;
+    p.nsplit = (int)(want > 1 ? want : 1);
+    p.grid = groups * p.nsplit;
+    const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    p.ml_off = up(kWsFixedBytes);
+    const size_t rows = p.nsplit > 1 ? (size_t)B * Hkv * p.nsplit * R : 0;
+    p.part_off = up(p.ml_off + 8 * rows);
+    p.ws_bytes = p.nsplit > 1 ? up(p.part_off + 4 * rows * p.dp) : kWsFixedBytes;
+    return p;
+}
+
+} // namespace rtopk
 
 extern "C" {
 
@@ -258,14 +298,14 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
     if (check_attention("tree attention", RTOPK_F16, B, N, Hq, Hkv, D, 1.f) != RTOPK_OK || N > rtopk::kMaxTree ||
         table_ld < 1 || page < 1 || !mul_fits(table_ld, page, INT_MAX - 4096))
         return 0;
-    return rtopk::kWsFixedBytes;
+    return rtopk::plan_attention(B, N, Hq, Hkv, D, table_ld * page).ws_bytes;
 }
 
 size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hkv, int D)
 {
     if (check_attention("cross attention", RTOPK_F16, B, N, Hq, Hkv, D, 1.f) != RTOPK_OK || S < 1 || S > INT_MAX - 4096)
         return 0;
-    return rtopk::kWsFixedBytes;
+    return rtopk::plan_attention(B, N, Hq, Hkv, D, S).ws_bytes;
 }
 
 int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, const void *v,
