@@ -64,12 +64,14 @@ struct AttnArgs {
     int row_tiles, nsplit, min_tiles;
     float *part;               // [B][Hkv][nsplit][N * G][dp] unnormalised outputs of the splits
     float *ml;                 // [B][Hkv][nsplit][N * G][2] their maxima (base 2) and sums
+    uint32_t *ticket;          // [B * Hkv] arrivals of attn_few's splits, zero between calls
 };
 
-// How a call is cut: workgroups of `waves` x 32 rows, tiles of `bn` keys,
-// heads padded to `dp` elements, keys in at most `nsplit` parts.
+// How a call is cut: workgroups of `waves` x 32 rows (few: of 16 or 32 rows,
+// by attn_few), tiles of `bn` keys, heads padded to `dp` elements, keys in at
+// most `nsplit` parts of at least min_tiles tiles.
 struct AttnPlan {
-    int dp, bn, waves, row_tiles, nsplit, min_tiles;
+    int few, dp, bn, waves, row_tiles, nsplit, min_tiles;
     int64_t grid;
     size_t ml_off, part_off, ws_bytes; // workspace behind the fixed region
 };

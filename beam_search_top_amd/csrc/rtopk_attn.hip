@@ -496,8 +496,457 @@ template <int DT, int DP, int WR, bool TREE> __global__ __launch_bounds__(64 * W
     }
 }
 
-// Joins the splits of a row in their order: a wave per row, four consecutive
-// elements per lane at a time.
+// The kernel of few rows (at most 16 NB per key head): a step of decoding, a
+// small tree. It is bound by reading keys and values once, so every load goes
+// to registers, coalesced, with as many bytes in flight as the registers
+// hold: each of the four waves takes every fourth step of 32 keys and refills
+// its key registers as soon as the scores are made and its value registers as
+// soon as the outputs are, without a barrier in the loop.
+//
+// v_mfma_f32_16x16x32 takes eight consecutive elements per lane of both
+// operands. X^T = K Q^T: lane l holds elements 32 c + 8 (l / 16) ... of key
+// l mod 16, as they lie in memory; the result holds keys 4 (l / 16) + i of row
+// l mod 16, which for two blocks of 16 keys is the B operand of O^T = V^T P^T
+// when the contraction goes over the keys in the order (l / 16, i, block). Its
+// A operand needs eight keys of one column per lane, while a load brings VE
+// consecutive columns of one key: lane l loads columns VE (l mod 16) ... of
+// its eight keys, and the VE products take column VE r + m as row r of product
+// m, each assembled by byte permutes (half an instruction per element).
+template <int DT> struct Small;
+template <> struct Small<1> {
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
+    {
+        typedef Elem<1>::V8 V8;
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+    }
+};
+template <> struct Small<2> {
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
+    {
+        typedef Elem<2>::V8 V8;
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+    }
+};
+
+// Maximum and sum over the four 16-lane rows of a wave.
+__device__ __forceinline__ float rows_max(float x)
+{
+    auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float rows_sum(float x)
+{
+    auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Data that another workgroup reads within the launch goes through the
+// device's coherence point (agent-scope accesses).
+__device__ __forceinline__ void put64(void *p, float x, float y)
+{
+    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    __hip_atomic_store(static_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get64(const void *p)
+{
+    return __hip_atomic_load(static_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+constexpr int kFewWaves = 4;
+constexpr int kFewStep = 32;   // keys per step of a wave
+constexpr int kFewSplits = 64; // splits at most
+
+template <int DT, int DP, int NB, bool TREE>
+__global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
+{
+    typedef Elem<DT> E;
+    typedef typename E::T T;
+    constexpr int VE = DP / 16, DC = DP / 32, VW = VE / 2; // columns per lane, products per score, value dwords
+    constexpr int PITCH = DP + 4;
+    __shared__ __align__(16) float s_o[kFewWaves * 16 * PITCH]; // the waves' outputs, a block of 16 rows at a time
+    __shared__ float s_m[kFewWaves][16 * NB], s_l[kFewWaves][16 * NB];
+    __shared__ int32_t s_parent[TREE ? 16 * NB : 1];
+    __shared__ uint32_t s_last;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, grp = lane >> 4;
+    int w = xcd_order((int)blockIdx.x, (int)gridDim.x);
+    const int split = w % a.nsplit;
+    w /= a.nsplit;
+    const int hk = w % a.Hkv, b = w / a.Hkv;
+    const KeyRange kr = key_range<TREE>(a, b);
+    const int R = kr.size * a.G;
+    const int tiles = (kr.end + kFewStep - 1) / kFewStep, per = tiles_per_split(tiles, a);
+    const int t_begin = split * per;
+    if (R == 0 || (split > 0 && t_begin >= tiles))
+        return;
+    const int t_end = t_begin + per < tiles ? t_begin + per : tiles;
+    const int parts = tiles > per ? (tiles + per - 1) / per : 1; // splits with keys
+
+    // ---- loads
+    const char *kbase = static_cast<const char *>(a.k) + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
+    const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
+    const char *zero = reinterpret_cast<const char *>(g_zeros);
+    // what decides about key t * 32 + lane mod 32, read ahead: its page, or its mask
+    auto fetch = [&](int t) -> int {
+        const int j = t * kFewStep + (lane & 31);
+        if (t >= t_end || j >= kr.end)
+            return -1;
+        if (TREE)
+            return a.table[(int64_t)b * a.ld + page_of(a.page, (uint32_t)j)];
+        return a.key_mask ? a.key_mask[(int64_t)b * a.S + j] : 0;
+    };
+    struct Step {
+        uint32_t oks;  // the keys that count
+        int64_t off;   // tree: byte offset of this lane's key
+    };
+    auto place = [&](int t, int info) -> Step {
+        const int j = t * kFewStep + (lane & 31);
+        bool ok = t < t_end && j < kr.end;
+        Step s{0, 0};
+        if (TREE) {
+            const int id = checked_page(info, a.num_pages);
+            ok = ok && id >= 0;
+            const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : 0));
+            s.off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : 0;
+        } else {
+            ok = ok && info == 0;
+        }
+        s.oks = (uint32_t)__ballot(ok);
+        return s;
+    };
+    auto row_off = [&](const Step &s, int t, int r, int64_t stride) -> int64_t {
+        if (TREE)
+            return (int64_t)((uint64_t)(uint32_t)__shfl((int)(s.off >> 32), r) << 32 | (uint32_t)__shfl((int)s.off, r));
+        return 2 * (int64_t)(t * kFewStep + r) * stride;
+    };
+    u32x4 kq[2][DC];
+    uint32_t vq[8][VW];
+    auto load_keys = [&](const Step &s, int t) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = 16 * k + col;
+            const char *p = kbase + row_off(s, t, r, a.ks[1]);
+            const bool in = s.oks >> r & 1;
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+                const int e = 32 * c + 8 * grp;
+                kq[k][c] = *reinterpret_cast<const u32x4 *>(in && e < a.D ? p + 2 * e : zero);
+            }
+        }
+    };
+    auto load_values = [&](const Step &s, int t) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 16 * (j / 4) + 4 * grp + j % 4;
+            const char *p = vbase + row_off(s, t, r, a.vs[1]);
+            p = (s.oks >> r & 1) && VE * col < a.D ? p + 2 * VE * col : zero;
+            if (VW == 4) {
+                const u32x4 y = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+                for (int x = 0; x < VW; ++x)
+                    vq[j][x] = y[x];
+            } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(p);
+                vq[j][0] = y.x;
+                vq[j][1] = y.y;
+            }
+        }
+    };
+    int t = t_begin + wave;
+    Step now = place(t, fetch(t));
+    load_keys(now, t);
+    int info = fetch(t + kFewWaves);
+    load_values(now, t);
+
+    // ---- this lane's query rows
+    u32x4 q[NB][DC];
+    int node[NB], head[NB];
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int row = 16 * n + col;
+        const bool live = row < R;
+        node[n] = live ? row / a.G : 0;
+        head[n] = hk * a.G + (live ? row - node[n] * a.G : 0);
+        const T *qp = static_cast<const T *>(a.q) + b * a.qs[0] + node[n] * a.qs[1] + head[n] * a.qs[2];
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+            const int e = 32 * c + 8 * grp;
+            u32x4 x = {0, 0, 0, 0};
+            if (live && e < a.D)
+                x = *reinterpret_cast<const u32x4 *>(qp + e);
+            q[n][c] = x ^ flip;
+        }
+    }
+    const float cs = fabsf(a.scale) * kLog2e;
+    // the nodes that each of its rows sees (at most 32 nodes: R <= 16 NB)
+    const bool walk = TREE && kr.size > 1 && t_end * kFewStep > kr.tree0;
+    uint32_t up[NB] = {};
+    if (TREE && walk) {
+        if (a.parents) {
+            if (tid < kr.size)
+                s_parent[tid] = parent_of(a.parents[(int64_t)b * a.N + tid], tid);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (a.parents)
+                for (int i = node[n]; i >= 0; i = s_parent[i])
+                    up[n] |= 1u << i;
+            else
+                up[n] = node[n] >= 31 ? ~0u : (1u << (node[n] + 1)) - 1;
+        }
+    }
+
+    f32x4 o[NB][VE];
+    float m[NB], l[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+#pragma unroll
+        for (int x = 0; x < VE; ++x)
+            o[n][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (; t < t_end; t += kFewWaves) {
+        const bool in_tree = walk && (t + 1) * kFewStep > kr.tree0;
+        const bool masked = now.oks != ~0u || in_tree;
+        // ---- scores
+        f32x4 x[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                x[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < DC; ++c)
+                    x[n][k] = Small<DT>::mfma(kq[k][c], q[n][c], x[n][k]);
+            }
+        const Step next = place(t + kFewWaves, info);
+        load_keys(next, t + kFewWaves);
+        info = fetch(t + 2 * kFewWaves);
+        // ---- weights
+        uint32_t see[NB];
+        u32x4 p[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            see[n] = now.oks;
+            if (in_tree) {
+                const int off = t * kFewStep - kr.tree0; // node of the step's first key: above -32
+                see[n] &= off < 0 ? (up[n] << -off) | ((1u << -off) - 1) : off < 32 ? up[n] >> off : 0;
+            }
+            const uint32_t bits = see[n] >> (4 * grp);
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[n][k][i] = bits >> (16 * k + i) & 1 ? x[n][k][i] : -INFINITY;
+            }
+            float mx = x[n][0][0];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx = fmaxf(mx, x[n][k][i]);
+            mx = rows_max(mx) * cs;
+            if (__any(mx > m[n] + kLazy)) {
+                const float mn = mx > m[n] ? mx : m[n];
+                const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+                m[n] = mn;
+                l[n] *= f;
+#pragma unroll
+                for (int y = 0; y < VE; ++y)
+                    o[n][y] *= f;
+            }
+            const float mu = m[n] == -INFINITY ? 0.f : m[n];
+            T y[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k][i], cs, -mu));
+                    if (masked && cs == 0.f) // 0 * -inf is not -inf
+                        e = bits >> (16 * k + i) & 1 ? e : 0.f;
+                    l[n] += e;
+                    y[4 * k + i] = (T)e;
+                }
+            p[n] = __builtin_bit_cast(u32x4, y);
+        }
+        // ---- a node's infinities and NaN, as in attn_tiles
+        bool odd = false;
+        if (TREE && in_tree) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < VW; ++e) {
+                    const bool lo = (vq[j][e] & E::kExp) == E::kExp, hi = (vq[j][e] >> 16 & E::kExp) == E::kExp;
+                    odd = odd || lo || hi;
+                    vq[j][e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                }
+            odd = __any(odd);
+        }
+        // ---- outputs
+#pragma unroll
+        for (int y = 0; y < VE; ++y) {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = __builtin_amdgcn_perm(vq[2 * j + 1][y / 2], vq[2 * j][y / 2], y % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                o[n][y] = Small<DT>::mfma(v, p[n], o[n][y]);
+        }
+        load_values(next, t + kFewWaves);
+        if (TREE && odd) {
+            for (int j = 0; j < kFewStep; ++j) {
+                if (!(now.oks >> j & 1))
+                    continue;
+                const int pos = t * kFewStep + j, pg = (int)page_of(a.page, (uint32_t)pos);
+                const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
+                const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int y = 0; y < VE; ++y) {
+                        const int e = VE * (4 * grp + i) + y;
+                        if (e >= a.D)
+                            continue;
+                        const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
+                        if ((raw & E::kExp) != E::kExp)
+                            continue;
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            if (see[n] >> j & 1)
+                                o[n][y][i] += (float)vr[e];
+                    }
+            }
+        }
+        now = next;
+    }
+
+    // ---- the waves' parts, joined in their order
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        l[n] = rows_sum(l[n]);
+        if (grp == 0) {
+            s_m[wave][16 * n + col] = m[n];
+            s_l[wave][16 * n + col] = l[n];
+        }
+    }
+    float *part = a.part + ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G * DP;
+    float *ml = a.ml + ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G * 2;
+    const int64_t step = (int64_t)a.N * a.G;
+    auto finish = [&](int row, int e, f32x4 y, float M, float L) {
+        const int nd = row / a.G, hd = hk * a.G + row - nd * a.G;
+        const int64_t at = ((int64_t)b * a.N + nd) * a.Hq + hd;
+        if (e < a.D) {
+            const float inv = 1.f / L;
+            T z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                z[i] = (T)(L == 0.f ? 0.f : y[i] * inv);
+            *reinterpret_cast<uint64_t *>(static_cast<T *>(a.out) + at * a.D + e) = __builtin_bit_cast(uint64_t, z);
+        }
+        if (a.lse && e == 0)
+            a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_log2f(L)) * kLn2;
+    };
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        __syncthreads();
+        float *mine = s_o + (wave * 16 + col) * PITCH + 4 * VE * grp;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int y = 0; y < VE; y += 4)
+                *reinterpret_cast<f32x4 *>(mine + VE * i + y) = f32x4{o[n][y][i], o[n][y + 1][i], o[n][y + 2][i], o[n][y + 3][i]};
+        __syncthreads();
+        for (int u = tid; u < 16 * DP / 4; u += 64 * kFewWaves) {
+            const int r = u / (DP / 4), e = u % (DP / 4) * 4, row = 16 * n + r;
+            if (row >= R)
+                continue;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int x = 0; x < kFewWaves; ++x)
+                M = fmaxf(M, s_m[x][row]);
+            const float mu = M == -INFINITY ? 0.f : M;
+            f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < kFewWaves; ++x) {
+                const float f = __builtin_amdgcn_exp2f(s_m[x][row] - mu);
+                L += f * s_l[x][row];
+                y += f * *reinterpret_cast<const f32x4 *>(s_o + (x * 16 + r) * PITCH + e);
+            }
+            if (parts == 1) {
+                finish(row, e, y, M, L);
+            } else {
+                float *to = part + (split * step + row) * DP + e;
+                put64(to, y[0], y[1]);
+                put64(to + 2, y[2], y[3]);
+                if (e == 0)
+                    put64(ml + 2 * (split * step + row), M, L);
+            }
+        }
+    }
+    if (parts == 1)
+        return;
+    // ---- the last workgroup of the group to arrive joins the splits, in their
+    // order whichever arrives last; the ticket is zero again afterwards
+    __builtin_amdgcn_s_waitcnt(0x0f70); // this wave's stores are done
+    __syncthreads();
+    uint32_t *ticket = a.ticket + b * a.Hkv + hk;
+    if (tid == 0) {
+        s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)parts - 1;
+        if (s_last)
+            __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last)
+        return;
+    for (int u = tid; u < R * (DP / 4); u += 64 * kFewWaves) {
+        const int row = u / (DP / 4), e = u % (DP / 4) * 4;
+        float M = -INFINITY, L = 0.f;
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        constexpr int AT = 8; // splits whose loads are in flight together
+        for (int s0 = 0; s0 < parts; s0 += AT) {
+            uint64_t h[AT], y0[AT], y1[AT];
+#pragma unroll
+            for (int x = 0; x < AT; ++x) {
+                const int sp = s0 + x < parts ? s0 + x : parts - 1;
+                h[x] = get64(ml + 2 * (sp * step + row));
+                y0[x] = get64(part + (sp * step + row) * DP + e);
+                y1[x] = get64(part + (sp * step + row) * DP + e + 2);
+            }
+            float Mn = M;
+#pragma unroll
+            for (int x = 0; x < AT; ++x)
+                Mn = fmaxf(Mn, __uint_as_float((uint32_t)h[x]));
+            const float mu = Mn == -INFINITY ? 0.f : Mn, f0 = __builtin_amdgcn_exp2f(M - mu);
+            L *= f0;
+            y *= f0;
+            M = Mn;
+#pragma unroll
+            for (int x = 0; x < AT; ++x) {
+                if (s0 + x >= parts)
+                    break;
+                const float f = __builtin_amdgcn_exp2f(__uint_as_float((uint32_t)h[x]) - mu);
+                L += f * __uint_as_float((uint32_t)(h[x] >> 32));
+                y[0] += f * __uint_as_float((uint32_t)y0[x]);
+                y[1] += f * __uint_as_float((uint32_t)(y0[x] >> 32));
+                y[2] += f * __uint_as_float((uint32_t)y1[x]);
+                y[3] += f * __uint_as_float((uint32_t)(y1[x] >> 32));
+            }
+        }
+        finish(row, e, y, M, L);
+    }
+}
+
+// Joins the splits of attn_tiles, in their order: a wave per row.
 template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int bn)
 {
     typedef typename Elem<DT>::T T;
@@ -514,15 +963,33 @@ template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn
     const int n = (tiles + per - 1) / per; // splits with keys
     const int64_t at0 = ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G + row, step = (int64_t)a.N * a.G;
     float M = -INFINITY, L = 0.f;
-    for (int s = 0; s < n; ++s)
-        M = fmaxf(M, a.ml[2 * (at0 + s * step)]);
-    const float mu = M == -INFINITY ? 0.f : M;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < n; ++s) {
-        const float f = __builtin_amdgcn_exp2f(a.ml[2 * (at0 + s * step)] - mu);
-        L += f * a.ml[2 * (at0 + s * step) + 1];
-        if (4 * lane < DP)
-            acc += f * *reinterpret_cast<const f32x4 *>(a.part + (at0 + s * step) * DP + 4 * lane);
+    constexpr int AT = 8; // splits whose loads are in flight together
+    for (int s0 = 0; s0 < n; s0 += AT) {
+        float2 h[AT];
+        f32x4 y[AT];
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            const int64_t at = at0 + (s0 + x < n ? s0 + x : n - 1) * step;
+            h[x] = *reinterpret_cast<const float2 *>(a.ml + 2 * at);
+            y[x] = *reinterpret_cast<const f32x4 *>(a.part + at * DP + (4 * lane < DP ? 4 * lane : 0));
+        }
+        float Mn = M;
+#pragma unroll
+        for (int x = 0; x < AT; ++x)
+            Mn = fmaxf(Mn, h[x].x);
+        const float mu = Mn == -INFINITY ? 0.f : Mn, f0 = __builtin_amdgcn_exp2f(M - mu);
+        L *= f0;
+        acc *= f0;
+        M = Mn;
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            if (s0 + x >= n)
+                break;
+            const float f = __builtin_amdgcn_exp2f(h[x].x - mu);
+            L += f * h[x].y;
+            acc += f * y[x];
+        }
     }
     const int node = row / a.G, head = hk * a.G + row - node * a.G;
     const int64_t at = ((int64_t)b * a.N + node) * a.Hq + head;
@@ -540,6 +1007,15 @@ template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn
 template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
 {
     const dim3 grid((unsigned)p.grid);
+    if constexpr (DP <= 128) {
+        if (p.few) {
+            if (p.few == 1)
+                hipLaunchKernelGGL((attn_few<DT, DP, 1, TREE>), grid, dim3(64 * kFewWaves), 0, s, a);
+            else
+                hipLaunchKernelGGL((attn_few<DT, DP, 2, TREE>), grid, dim3(64 * kFewWaves), 0, s, a);
+            return hipGetLastError();
+        }
+    }
     if (p.waves == 1)
         hipLaunchKernelGGL((attn_tiles<DT, DP, 1, TREE>), grid, dim3(64), 0, s, a);
     else if (p.waves == 2)

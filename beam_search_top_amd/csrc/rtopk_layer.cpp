@@ -102,6 +102,7 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
     const auto go = [&](void *ws) {
         a.ml = ws ? (float *)((uint8_t *)ws + p.ml_off) : nullptr;
         a.part = ws ? (float *)((uint8_t *)ws + p.part_off) : nullptr;
+        a.ticket = ws ? (uint32_t *)((uint8_t *)ws + rtopk::kWsTicketOff) : nullptr;
         const hipError_t e = rtopk::launch_attention(a, p, dtype, tree, stream);
         if (e != hipSuccess)
             return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
@@ -120,15 +121,17 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S)
 {
     AttnPlan p{};
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    p.bn = p.dp > 128 ? 32 : 64;
     const int64_t R = (int64_t)N * (Hq / Hkv);
-    p.waves = R <= 32 ? 1 : R <= 64 ? 2 : 4;
-    p.row_tiles = (int)((R + 32 * p.waves - 1) / (32 * p.waves));
+    p.few = p.dp <= 128 && R <= 32 ? (R <= 16 ? 1 : 2) : 0;
+    p.bn = p.few || p.dp > 128 ? 32 : 64;
+    p.waves = p.few ? 4 : R <= 32 ? 1 : R <= 64 ? 2 : 4;
+    p.row_tiles = p.few ? 1 : (int)((R + 32 * p.waves - 1) / (32 * p.waves));
     const int64_t groups = (int64_t)B * Hkv * p.row_tiles, tiles = ((int64_t)S + p.bn - 1) / p.bn;
-    p.min_tiles = 4;
-    int64_t want = (512 + groups - 1) / groups; // two workgroups per CU
+    p.min_tiles = p.few ? 8 : 4;
+    int64_t want = ((p.few ? 768 : 512) + groups - 1) / groups;
     const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
     want = want < most ? want : most;
+    want = p.few && want > 64 ? 64 : want;
     p.nsplit = (int)(want > 1 ? want : 1);
     p.grid = groups * p.nsplit;
     const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
