@@ -23,6 +23,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
+// Global memory by its address space: a pointer that may be one of two others'
+// would else be loaded from as a generic one, which LDS waits wait for too.
+typedef const __attribute__((address_space(1))) char gchar;
+typedef const __attribute__((address_space(1))) u32x4 gu32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef const __attribute__((address_space(1))) u32x2 gu32x2;
 
 // The 16-bit types: 1 float16, 2 bfloat16.
 template <int DT> struct Elem;
@@ -116,7 +122,8 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // unrounded ones, in float32.
 constexpr float kLazy = 8.f;
 
-template <int DT, int DP, int WR, bool TREE> __global__ __launch_bounds__(64 * WR) void attn_tiles(const AttnArgs a)
+template <int DT, int DP, int WR, bool TREE>
+__global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const AttnArgs a)
 {
     typedef Elem<DT> E;
     typedef typename E::T T;
@@ -561,7 +568,7 @@ constexpr int kFewStep = 32;   // keys per step of a wave
 constexpr int kFewSplits = 64; // splits at most
 
 template <int DT, int DP, int NB, bool TREE>
-__global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 {
     typedef Elem<DT> E;
     typedef typename E::T T;
@@ -588,9 +595,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
     const int parts = tiles > per ? (tiles + per - 1) / per : 1; // splits with keys
 
     // ---- loads
-    const char *kbase = static_cast<const char *>(a.k) + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
-    const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
-    const char *zero = reinterpret_cast<const char *>(g_zeros);
+    gchar *kbase = (gchar *)a.k + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
+    gchar *vbase = (gchar *)a.v + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
+    gchar *zero = (gchar *)g_zeros;
     // what decides about key t * 32 + lane mod 32, read ahead: its page, or its mask
     auto fetch = [&](int t) -> int {
         const int j = t * kFewStep + (lane & 31);
@@ -630,12 +637,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int r = 16 * k + col;
-            const char *p = kbase + row_off(s, t, r, a.ks[1]);
+            gchar *p = kbase + row_off(s, t, r, a.ks[1]);
             const bool in = s.oks >> r & 1;
 #pragma unroll
             for (int c = 0; c < DC; ++c) {
                 const int e = 32 * c + 8 * grp;
-                kq[k][c] = *reinterpret_cast<const u32x4 *>(in && e < a.D ? p + 2 * e : zero);
+                kq[k][c] = *(gu32x4 *)(in && e < a.D ? p + 2 * e : zero);
             }
         }
     };
@@ -643,17 +650,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int r = 16 * (j / 4) + 4 * grp + j % 4;
-            const char *p = vbase + row_off(s, t, r, a.vs[1]);
+            gchar *p = vbase + row_off(s, t, r, a.vs[1]);
             p = (s.oks >> r & 1) && VE * col < a.D ? p + 2 * VE * col : zero;
             if (VW == 4) {
-                const u32x4 y = *reinterpret_cast<const u32x4 *>(p);
+                const u32x4 y = *(gu32x4 *)p;
 #pragma unroll
                 for (int x = 0; x < VW; ++x)
                     vq[j][x] = y[x];
             } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(p);
-                vq[j][0] = y.x;
-                vq[j][1] = y.y;
+                const u32x2 y = *(gu32x2 *)p;
+                vq[j][0] = y[0];
+                vq[j][1] = y[1];
             }
         }
     };
@@ -809,7 +816,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attn_few(const AttnArgs a)
                     continue;
                 const int pos = t * kFewStep + j, pg = (int)page_of(a.page, (uint32_t)pos);
                 const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
-                const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+                const T *vr = static_cast<const T *>(a.v) + hk * a.vs[2] + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
