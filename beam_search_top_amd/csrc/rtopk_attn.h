@@ -42,6 +42,7 @@ hipError_t launch_cache_store(StoreArgs a, int unit_bytes, hipStream_t s);
 
 constexpr int kMaxTree = 256;   // nodes of a tree
 constexpr int kMaxHeadDim = 256;
+constexpr int kMaxParts = 64;   // shares of a batch element in attn_few
 
 // Attention of N query rows per batch element over its keys (rtopk_attn.hip).
 struct AttnArgs {
@@ -62,20 +63,22 @@ struct AttnArgs {
     float *lse;                // [B][N][Hq] or null
     // the split over workgroups (plan_attention)
     int row_tiles, nsplit, min_tiles;
-    float *part;               // [B][Hkv][nsplit][N * G][dp] unnormalised outputs of the splits
-    float *ml;                 // [B][Hkv][nsplit][N * G][2] their maxima (base 2) and sums
-    uint32_t *ticket;          // [B * Hkv] arrivals of attn_few's splits, zero between calls
+    int units;                 // attn_few: shares of all batch elements at most, 0 = one each
+    float *part;               // [B][Hkv][nsplit][N * G][dp] (attn_few: [units][Hkv][N * G][dp]) unnormalised outputs
+    float *ml;                 // the same with [2] for [dp]: their maxima (base 2) and sums
+    uint32_t *ticket;          // [B * Hkv] arrivals of attn_few's shares, zero between calls
 };
 
 // How a call is cut: workgroups of `waves` x 32 rows (few: of 16 or 32 rows,
 // by attn_few), tiles of `bn` keys, heads padded to `dp` elements, keys in at
-// most `nsplit` parts of at least min_tiles tiles.
+// most `nsplit` parts of at least min_tiles tiles (attn_few: in `units` shares).
 struct AttnPlan {
-    int few, dp, bn, waves, row_tiles, nsplit, min_tiles;
+    int few, dp, bn, waves, row_tiles, nsplit, min_tiles, units;
     int64_t grid;
     size_t ml_off, part_off, ws_bytes; // workspace behind the fixed region
 };
-AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S);
+// wide: rows of keys or values lie 2^25 elements or more apart (not for attn_few)
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide);
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s);
 
 // Calls `launch` with a library-owned workspace of `need` bytes for `stream`

@@ -504,21 +504,24 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
 }
 
 // The kernel of few rows (at most 16 NB per key head): a step of decoding, a
-// small tree. It is bound by reading keys and values once, so every load goes
-// to registers, coalesced, with as many bytes in flight as the registers
-// hold: each of the four waves takes every fourth step of 32 keys and refills
-// its key registers as soon as the scores are made and its value registers as
-// soon as the outputs are, without a barrier in the loop.
+// small tree. It is bound by reading keys and values once, so what counts is
+// bytes in flight, whole lines per load and even shares: every wave takes
+// steps of 32 keys of its own, loads whole rows to registers, and refills the
+// key registers as soon as the keys are in LDS and the value registers as soon
+// as the outputs are made, without a barrier in the loop (the LDS that turns
+// key rows into operands is the wave's own). All loads are non-temporal:
+// nobody reads the data again.
 //
 // v_mfma_f32_16x16x32 takes eight consecutive elements per lane of both
-// operands. X^T = K Q^T: lane l holds elements 32 c + 8 (l / 16) ... of key
-// l mod 16, as they lie in memory; the result holds keys 4 (l / 16) + i of row
-// l mod 16, which for two blocks of 16 keys is the B operand of O^T = V^T P^T
-// when the contraction goes over the keys in the order (l / 16, i, block). Its
-// A operand needs eight keys of one column per lane, while a load brings VE
-// consecutive columns of one key: lane l loads columns VE (l mod 16) ... of
-// its eight keys, and the VE products take column VE r + m as row r of product
-// m, each assembled by byte permutes (half an instruction per element).
+// operands. X^T = K Q^T: the A operand's row r is key 16 k + 4 (r mod 4) + r / 4
+// of block k, so that lane l, which holds rows 4 (l / 16) + i of the result,
+// holds keys 4 i + l / 16 of each block: the B operand of O^T = V^T P^T when the
+// contraction goes over the keys in the order (l / 16, block, i). The A operand
+// there needs eight keys of one column per lane, while a load brings VE
+// consecutive columns of one key: lane l loads columns VE (l mod 16) ... of its
+// eight keys (so that load j of a wave is the four whole rows 4 j ... 4 j + 3), and
+// the VE products take column VE r + m as row r of product m, each assembled
+// by byte permutes (half an instruction per element).
 template <int DT> struct Small;
 template <> struct Small<1> {
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
@@ -564,56 +567,156 @@ __device__ __forceinline__ uint64_t get64(const void *p)
 }
 
 constexpr int kFewWaves = 4;
-constexpr int kFewStep = 32;   // keys per step of a wave
-constexpr int kFewSplits = 64; // splits at most
+constexpr int kFewStep = 32; // keys per step of a wave
 
-template <int DT, int DP, int NB, bool TREE>
+// A workgroup's share: steps [begin, end) of batch element b, one of `parts`
+// shares of it; `unit` numbers the shares of all batch elements, `unit0` is
+// that of b's first.
+struct Share {
+    int b, begin, end, parts, unit, unit0;
+};
+
+// Cuts the steps of all batch elements into shares of equal size, `units` of
+// them at most: long and short batch elements load the GPU evenly, which the host
+// cannot do without knowing the lengths. Every wave sums the lengths by itself
+// (B <= 256). A batch element with rows has at least one share.
+template <bool TREE> __device__ __forceinline__ Share find_share(const AttnArgs &a, int unit, int lane)
+{
+    Share s{-1, 0, 0, 0, unit, 0};
+    int tiles[4], total = 0, longest = 0;
+    const int chunks = (a.B + 63) / 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        tiles[i] = -1; // no rows: no share
+        if (i >= chunks)
+            continue;
+        const int b = 64 * i + lane;
+        if (b < a.B) {
+            const KeyRange kr = key_range<TREE>(a, b);
+            if (kr.size > 0)
+                tiles[i] = (kr.end + kFewStep - 1) / kFewStep;
+        }
+        total += tiles[i] > 0 ? tiles[i] : 0; // at most 256 * 2^26 / 32 per lane group: the host bounds B * S
+        longest = tiles[i] > longest ? tiles[i] : longest;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        total += __shfl_xor(total, o);
+        const int x = __shfl_xor(longest, o);
+        longest = x > longest ? x : longest;
+    }
+    const int room = a.units - a.B; // shares besides each batch element's last, partial one
+    int quota = (total + room - 1) / room;
+    quota = quota > a.min_tiles ? quota : a.min_tiles;
+    const int most = (longest + kMaxParts - 1) / kMaxParts;
+    quota = quota > most ? quota : most;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i >= chunks)
+            break;
+        const int n = tiles[i] < 0 ? 0 : tiles[i] <= quota ? 1 : (tiles[i] + quota - 1) / quota;
+        int pre = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(pre, o);
+            pre += lane >= o ? x : 0;
+        }
+        pre += before;
+        const uint64_t hit = __ballot(unit < pre && unit >= pre - n);
+        if (hit) {
+            const int src = __ffsll((unsigned long long)hit) - 1;
+            const int t = __builtin_amdgcn_readlane(tiles[i], src);
+            s.b = 64 * i + src;
+            s.parts = __builtin_amdgcn_readlane(n, src);
+            s.unit0 = __builtin_amdgcn_readlane(pre, src) - s.parts;
+            s.begin = (unit - s.unit0) * quota;
+            s.end = s.begin + quota < t ? s.begin + quota : t;
+            return s;
+        }
+        before = __builtin_amdgcn_readlane(pre, 63);
+    }
+    return s;
+}
+
+// MODE 0: cross attention; 1: a tree, pages of a multiple of 8 tokens; 2: a tree, other pages.
+// (Modes of one kernel, not branches in it: the counts by which a wave waits for
+// its older loads only must be the same on every path.)
+template <int DT, int DP, int NB, int MODE>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 {
+    constexpr bool TREE = MODE != 0;
     typedef Elem<DT> E;
     typedef typename E::T T;
     constexpr int VE = DP / 16, DC = DP / 32, VW = VE / 2; // columns per lane, products per score, value dwords
+    constexpr int ROWB = DP * 2, CH = DP / 8, RPL = 1024 / ROWB, NK = kFewStep / RPL; // a 1 KiB load is RPL rows
+    constexpr int FK = CH < 16 ? CH - 1 : 15;
     constexpr int PITCH = DP + 4;
-    __shared__ __align__(16) float s_o[kFewWaves * 16 * PITCH]; // the waves' outputs, a block of 16 rows at a time
+    constexpr int KEYS = kFewWaves * kFewStep * ROWB, OUTS = kFewWaves * 16 * PITCH * 4;
+    // the waves' keys; after the loop their outputs, a block of 16 rows at a time
+    __shared__ __align__(1024) uint8_t smem[KEYS > OUTS ? KEYS : OUTS];
     __shared__ float s_m[kFewWaves][16 * NB], s_l[kFewWaves][16 * NB];
     __shared__ int32_t s_parent[TREE ? 16 * NB : 1];
     __shared__ uint32_t s_last;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, grp = lane >> 4;
-    int w = xcd_order((int)blockIdx.x, (int)gridDim.x);
-    const int split = w % a.nsplit;
-    w /= a.nsplit;
-    const int hk = w % a.Hkv, b = w / a.Hkv;
+    // workgroup w runs on XCD w mod 8: shares go around the XCDs, and all key
+    // heads of a share, which lie side by side in memory, to the same one
+    const int xi = (int)blockIdx.x / 8, hk = xi % a.Hkv, unit = xi / a.Hkv * 8 + (int)blockIdx.x % 8;
+    Share sh;
+    if (a.units > 0) {
+        sh = find_share<TREE>(a, unit, lane);
+        if (sh.b < 0)
+            return;
+    } else {
+        if (unit >= a.B)
+            return;
+        sh = Share{unit, 0, 0, 1, unit, unit};
+    }
+    // the same for every lane, which the compiler does not see through the search
+    sh.begin = __builtin_amdgcn_readfirstlane(sh.begin);
+    sh.end = __builtin_amdgcn_readfirstlane(sh.end);
+    sh.parts = __builtin_amdgcn_readfirstlane(sh.parts);
+    sh.unit0 = __builtin_amdgcn_readfirstlane(sh.unit0);
+    const int b = __builtin_amdgcn_readfirstlane(sh.b);
     const KeyRange kr = key_range<TREE>(a, b);
     const int R = kr.size * a.G;
-    const int tiles = (kr.end + kFewStep - 1) / kFewStep, per = tiles_per_split(tiles, a);
-    const int t_begin = split * per;
-    if (R == 0 || (split > 0 && t_begin >= tiles))
+    if (R == 0)
         return;
-    const int t_end = t_begin + per < tiles ? t_begin + per : tiles;
-    const int parts = tiles > per ? (tiles + per - 1) / per : 1; // splits with keys
+    const int t_begin = sh.begin, t_end = a.units > 0 ? sh.end : (kr.end + kFewStep - 1) / kFewStep, parts = sh.parts;
 
     // ---- loads
     gchar *kbase = (gchar *)a.k + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
     gchar *vbase = (gchar *)a.v + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
-    gchar *zero = (gchar *)g_zeros;
-    // what decides about key t * 32 + lane mod 32, read ahead: its page, or its mask
+    uint8_t *mine = smem + wave * kFewStep * ROWB;
+    // Step t is rows first(t) ... + 31. Past the last row that can be read (cross: S
+    // >= 32) it begins earlier and leaves out the keys of the step before.
+    auto first = [&](int t) -> int {
+        if (TREE)
+            return t * kFewStep;
+        const int f = (t < t_end ? t : t_begin) * kFewStep;
+        return f < a.S - kFewStep ? f : a.S - kFewStep;
+    };
+    // what decides about key first(t) + lane mod 32, read ahead: its page, or its mask
     auto fetch = [&](int t) -> int {
-        const int j = t * kFewStep + (lane & 31);
+        const int j = first(t) + (lane & 31);
         if (t >= t_end || j >= kr.end)
             return -1;
         if (TREE)
             return a.table[(int64_t)b * a.ld + page_of(a.page, (uint32_t)j)];
         return a.key_mask ? a.key_mask[(int64_t)b * a.S + j] : 0;
     };
+    // Keys that do not count are loaded all the same, from some place that can
+    // be read (tree: the cache's first rows); their scores are replaced and their
+    // values zeroed where they are used.
     struct Step {
-        uint32_t oks;  // the keys that count
-        int64_t off;   // tree: byte offset of this lane's key
+        uint32_t oks; // the keys that count
+        int64_t off;  // tree: byte offset of this lane's key
     };
     auto place = [&](int t, int info) -> Step {
-        const int j = t * kFewStep + (lane & 31);
-        bool ok = t < t_end && j < kr.end;
+        const int j = first(t) + (lane & 31);
+        bool ok = t < t_end && j >= t * kFewStep && j < kr.end;
         Step s{0, 0};
         if (TREE) {
             const int id = checked_page(info, a.num_pages);
@@ -626,39 +729,43 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
         s.oks = (uint32_t)__ballot(ok);
         return s;
     };
-    auto row_off = [&](const Step &s, int t, int r, int64_t stride) -> int64_t {
-        if (TREE)
-            return (int64_t)((uint64_t)(uint32_t)__shfl((int)(s.off >> 32), r) << 32 | (uint32_t)__shfl((int)s.off, r));
-        return 2 * (int64_t)(t * kFewStep + r) * stride;
+    // Row u + lane_r of a step (u the same for the wave) lies at a base of the wave's and a
+    // 32-bit offset of the lane's: cross attention's rows are evenly spaced (the
+    // host sees to it that 32 of them span less than 2^32 bytes), up to 8 rows of a tree lie on
+    // one page where pages allow it. Else every lane has a 64-bit offset of its own.
+    const int lrow = lane / CH, lchunk = lane % CH;
+    const uint32_t kstep = 2 * (uint32_t)a.ks[1], vstep = 2 * (uint32_t)a.vs[1];
+    const uint32_t kcol = lchunk * 8 < a.D ? lchunk * 16 : 0, vcol = VE * col < a.D ? 2 * VE * col : 0;
+    const uint32_t klane = lrow * kstep + kcol, vlane = grp * vstep + vcol;
+    auto row = [&](gchar *base, const Step &s, int t, int u, int lane_r, uint32_t step, uint32_t lane_off, uint32_t lane_col) -> gchar * {
+        // behind the last step, every lane reads the same line
+        if constexpr (MODE == 0)
+            return base + (t < t_end ? (int64_t)(first(t) + u) * step : 0) + (t < t_end ? lane_off : 0);
+        else if constexpr (MODE == 1)
+            return base + (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(s.off >> 32), u) << 32 |
+                                    (uint32_t)__builtin_amdgcn_readlane((int)s.off, u)) + (t < t_end ? lane_off : 0);
+        else
+            return base + (int64_t)((uint64_t)(uint32_t)__shfl((int)(s.off >> 32), u + lane_r) << 32 |
+                                    (uint32_t)__shfl((int)s.off, u + lane_r)) + (t < t_end ? lane_col : 0);
     };
-    u32x4 kq[2][DC];
-    uint32_t vq[8][VW];
+    u32x4 kq[NK];
     auto load_keys = [&](const Step &s, int t) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = 16 * k + col;
-            gchar *p = kbase + row_off(s, t, r, a.ks[1]);
-            const bool in = s.oks >> r & 1;
-#pragma unroll
-            for (int c = 0; c < DC; ++c) {
-                const int e = 32 * c + 8 * grp;
-                kq[k][c] = *(gu32x4 *)(in && e < a.D ? p + 2 * e : zero);
-            }
-        }
+        for (int i = 0; i < NK; ++i)
+            kq[i] = __builtin_nontemporal_load((gu32x4 *)row(kbase, s, t, i * RPL, lrow, kstep, klane, kcol));
     };
+    uint32_t vq[8][VW];
     auto load_values = [&](const Step &s, int t) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int r = 16 * (j / 4) + 4 * grp + j % 4;
-            gchar *p = vbase + row_off(s, t, r, a.vs[1]);
-            p = (s.oks >> r & 1) && VE * col < a.D ? p + 2 * VE * col : zero;
-            if (VW == 4) {
-                const u32x4 y = *(gu32x4 *)p;
+            gchar *p = row(vbase, s, t, 4 * j, grp, vstep, vlane, vcol);
+            if constexpr (VW == 4) {
+                const u32x4 y = __builtin_nontemporal_load((gu32x4 *)p);
 #pragma unroll
                 for (int x = 0; x < VW; ++x)
                     vq[j][x] = y[x];
             } else {
-                const u32x2 y = *(gu32x2 *)p;
+                const u32x2 y = __builtin_nontemporal_load((gu32x2 *)p);
                 vq[j][0] = y[0];
                 vq[j][1] = y[1];
             }
@@ -680,13 +787,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
         const bool live = row < R;
         node[n] = live ? row / a.G : 0;
         head[n] = hk * a.G + (live ? row - node[n] * a.G : 0);
-        const T *qp = static_cast<const T *>(a.q) + b * a.qs[0] + node[n] * a.qs[1] + head[n] * a.qs[2];
+        gchar *qp = (gchar *)a.q + 2 * (b * a.qs[0] + node[n] * a.qs[1] + head[n] * a.qs[2]);
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
             const int e = 32 * c + 8 * grp;
             u32x4 x = {0, 0, 0, 0};
             if (live && e < a.D)
-                x = *reinterpret_cast<const u32x4 *>(qp + e);
+                x = *(gu32x4 *)(qp + 2 * e);
             q[n][c] = x ^ flip;
         }
     }
@@ -709,6 +816,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
                 up[n] = node[n] >= 31 ? ~0u : (1u << (node[n] + 1)) - 1;
         }
     }
+    // this lane's key in each block, as the A operand's row col
+    const int kr0 = 4 * (col & 3) + (col >> 2);
 
     f32x4 o[NB][VE];
     float m[NB], l[NB];
@@ -724,19 +833,39 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
         const bool in_tree = walk && (t + 1) * kFewStep > kr.tree0;
         const bool masked = now.oks != ~0u || in_tree;
         // ---- scores
-        f32x4 x[NB][2];
+        if (a.D < DP) { // elements past the head's are zeros in both operands
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+            for (int i = 0; i < NK; ++i)
+                kq[i] = lchunk * 8 < a.D ? kq[i] : u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                x[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < DC; ++c)
-                    x[n][k] = Small<DT>::mfma(kq[k][c], q[n][c], x[n][k]);
-            }
+        for (int i = 0; i < NK; ++i) {
+            const int r = i * RPL + lrow;
+            *reinterpret_cast<u32x4 *>(mine + r * ROWB + (lchunk ^ (r & FK)) * 16) = kq[i];
+        }
         const Step next = place(t + kFewWaves, info);
         load_keys(next, t + kFewWaves);
         info = fetch(t + 2 * kFewWaves);
+        // this wave's own LDS, which serves it in order: no other wave to wait for
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        f32x4 x[NB][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = 16 * k + kr0;
+            u32x4 kf[DC];
+#pragma unroll
+            for (int c = 0; c < DC; ++c)
+                kf[c] = *reinterpret_cast<const u32x4 *>(mine + r * ROWB + ((4 * c + grp) ^ (r & FK)) * 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                x[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < DC; ++c)
+                    x[n][k] = Small<DT>::mfma(kf[c], q[n][c], x[n][k]);
+            }
+        }
         // ---- weights
         uint32_t see[NB];
         u32x4 p[NB];
@@ -747,13 +876,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
                 const int off = t * kFewStep - kr.tree0; // node of the step's first key: above -32
                 see[n] &= off < 0 ? (up[n] << -off) | ((1u << -off) - 1) : off < 32 ? up[n] >> off : 0;
             }
-            const uint32_t bits = see[n] >> (4 * grp);
+            const uint32_t bits = see[n] >> grp;
             if (masked) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[n][k][i] = bits >> (16 * k + i) & 1 ? x[n][k][i] : -INFINITY;
+                        x[n][k][i] = bits >> (16 * k + 4 * i) & 1 ? x[n][k][i] : -INFINITY;
             }
             float mx = x[n][0][0];
 #pragma unroll
@@ -779,11 +908,18 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
                 for (int i = 0; i < 4; ++i) {
                     float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k][i], cs, -mu));
                     if (masked && cs == 0.f) // 0 * -inf is not -inf
-                        e = bits >> (16 * k + i) & 1 ? e : 0.f;
+                        e = bits >> (16 * k + 4 * i) & 1 ? e : 0.f;
                     l[n] += e;
                     y[4 * k + i] = (T)e;
                 }
             p[n] = __builtin_bit_cast(u32x4, y);
+        }
+        if (now.oks != ~0u) { // 0 * infinity: a value that does not count must be finite
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < VW; ++e)
+                    vq[j][e] = now.oks >> (4 * j + grp) & 1 ? vq[j][e] : 0u;
         }
         // ---- a node's infinities and NaN, as in attn_tiles
         bool odd = false;
@@ -846,9 +982,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             s_l[wave][16 * n + col] = l[n];
         }
     }
-    float *part = a.part + ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G * DP;
-    float *ml = a.ml + ((int64_t)b * a.Hkv + hk) * a.nsplit * a.N * a.G * 2;
-    const int64_t step = (int64_t)a.N * a.G;
+    float *s_o = reinterpret_cast<float *>(smem);
+    const int64_t step = (int64_t)a.Hkv * a.N * a.G; // rows of a unit
+    float *part = a.part + (sh.unit0 * step + (int64_t)hk * a.N * a.G) * DP;
+    float *ml = a.ml + (sh.unit0 * step + (int64_t)hk * a.N * a.G) * 2;
+    const int split = sh.unit - sh.unit0;
     auto finish = [&](int row, int e, f32x4 y, float M, float L) {
         const int nd = row / a.G, hd = hk * a.G + row - nd * a.G;
         const int64_t at = ((int64_t)b * a.N + nd) * a.Hq + hd;
@@ -866,12 +1004,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         __syncthreads();
-        float *mine = s_o + (wave * 16 + col) * PITCH + 4 * VE * grp;
+        float *to = s_o + (wave * 16 + col) * PITCH + 4 * VE * grp;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int y = 0; y < VE; y += 4)
-                *reinterpret_cast<f32x4 *>(mine + VE * i + y) = f32x4{o[n][y][i], o[n][y + 1][i], o[n][y + 2][i], o[n][y + 3][i]};
+                *reinterpret_cast<f32x4 *>(to + VE * i + y) = f32x4{o[n][y][i], o[n][y + 1][i], o[n][y + 2][i], o[n][y + 3][i]};
         __syncthreads();
         for (int u = tid; u < 16 * DP / 4; u += 64 * kFewWaves) {
             const int r = u / (DP / 4), e = u % (DP / 4) * 4, row = 16 * n + r;
@@ -1016,10 +1154,22 @@ template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, c
     const dim3 grid((unsigned)p.grid);
     if constexpr (DP <= 128) {
         if (p.few) {
-            if (p.few == 1)
-                hipLaunchKernelGGL((attn_few<DT, DP, 1, TREE>), grid, dim3(64 * kFewWaves), 0, s, a);
-            else
-                hipLaunchKernelGGL((attn_few<DT, DP, 2, TREE>), grid, dim3(64 * kFewWaves), 0, s, a);
+            const dim3 block(64 * kFewWaves);
+            if constexpr (TREE) {
+                const bool even = a.page.d % 8 == 0;
+                if (p.few == 1 && even)
+                    hipLaunchKernelGGL((attn_few<DT, DP, 1, 1>), grid, block, 0, s, a);
+                else if (p.few == 1)
+                    hipLaunchKernelGGL((attn_few<DT, DP, 1, 2>), grid, block, 0, s, a);
+                else if (even)
+                    hipLaunchKernelGGL((attn_few<DT, DP, 2, 1>), grid, block, 0, s, a);
+                else
+                    hipLaunchKernelGGL((attn_few<DT, DP, 2, 2>), grid, block, 0, s, a);
+            } else if (p.few == 1) {
+                hipLaunchKernelGGL((attn_few<DT, DP, 1, 0>), grid, block, 0, s, a);
+            } else {
+                hipLaunchKernelGGL((attn_few<DT, DP, 2, 0>), grid, block, 0, s, a);
+            }
             return hipGetLastError();
         }
     }

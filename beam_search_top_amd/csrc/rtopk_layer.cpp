@@ -85,10 +85,20 @@ int check_attention(const char *what, int dtype, int B, int N, int Hq, int Hkv, 
     return RTOPK_OK;
 }
 
+// Workspace of a call whatever its strides.
+size_t attention_bytes(int B, int N, int Hq, int Hkv, int D, int S)
+{
+    const size_t x = rtopk::plan_attention(B, N, Hq, Hkv, D, S, false).ws_bytes;
+    const size_t y = rtopk::plan_attention(B, N, Hq, Hkv, D, S, true).ws_bytes;
+    return x > y ? x : y;
+}
+
 int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree, void *workspace, size_t ws_bytes,
                       hipStream_t stream)
 {
-    const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S);
+    // attn_few holds the offsets of 32 rows in 32 bits, and needs 32 rows to read
+    const bool wide = a.ks[1] >= (1 << 25) || a.vs[1] >= (1 << 25) || (!tree && a.S < 32);
+    const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S, wide);
     if (workspace && (uintptr_t)workspace % 256)
         return set_error(RTOPK_EINVAL, "%s: workspace is not 256-byte aligned", what);
     if (workspace && ws_bytes < p.ws_bytes)
@@ -99,6 +109,7 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
     a.min_tiles = p.min_tiles;
+    a.units = p.units;
     const auto go = [&](void *ws) {
         a.ml = ws ? (float *)((uint8_t *)ws + p.ml_off) : nullptr;
         a.part = ws ? (float *)((uint8_t *)ws + p.part_off) : nullptr;
@@ -108,37 +119,57 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
             return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
         return (int)RTOPK_OK;
     };
-    if (p.nsplit == 1 || workspace)
-        return go(p.nsplit == 1 ? nullptr : workspace);
+    if (p.ws_bytes == rtopk::kWsFixedBytes || workspace)
+        return go(workspace);
     return rtopk::with_workspace(p.ws_bytes, stream, go);
 }
 
 } // namespace
 
+#ifndef FEW_MIN
+#define FEW_MIN 4
+#define FEW_S64 1024
+#define FEW_S128 512
+#define FEW_MULT 0
+#endif
 namespace rtopk {
 
-AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S)
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
 {
     AttnPlan p{};
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
     const int64_t R = (int64_t)N * (Hq / Hkv);
-    p.few = p.dp <= 128 && R <= 32 ? (R <= 16 ? 1 : 2) : 0;
+    p.few = p.dp <= 128 && R <= 32 && !wide ? (R <= 16 ? 1 : 2) : 0;
     p.bn = p.few || p.dp > 128 ? 32 : 64;
     p.waves = p.few ? 4 : R <= 32 ? 1 : R <= 64 ? 2 : 4;
     p.row_tiles = p.few ? 1 : (int)((R + 32 * p.waves - 1) / (32 * p.waves));
     const int64_t groups = (int64_t)B * Hkv * p.row_tiles, tiles = ((int64_t)S + p.bn - 1) / p.bn;
-    p.min_tiles = p.few ? 8 : 4;
-    int64_t want = ((p.few ? 768 : 512) + groups - 1) / groups;
-    const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
-    want = want < most ? want : most;
-    want = p.few && want > 64 ? 64 : want;
-    p.nsplit = (int)(want > 1 ? want : 1);
-    p.grid = groups * p.nsplit;
     const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    p.nsplit = 1;
     p.ml_off = up(kWsFixedBytes);
-    const size_t rows = p.nsplit > 1 ? (size_t)B * Hkv * p.nsplit * R : 0;
+    size_t rows = 0; // rows of partial outputs
+    if (p.few) {
+        // Shares for every place on the GPU (3 workgroups per CU, 4 at D <= 64), and
+        // several per batch element when there are many of those
+        p.min_tiles = FEW_MIN;
+        int64_t units = ((p.dp == 64 ? FEW_S64 : FEW_S128) + Hkv - 1) / Hkv;
+        units = units > (FEW_MULT > 0 ? FEW_MULT : 2) * B ? units : (FEW_MULT > 0 ? FEW_MULT : 2) * B;
+        const bool cut = tiles > p.min_tiles && (FEW_MULT > 0 || (int64_t)B * Hkv < (p.dp == 64 ? FEW_S64 : FEW_S128)) && B <= 256 && (int64_t)B * Hkv <= kTicketCap && (int64_t)B * tiles <= (1 << 30) &&
+                         units <= (1 << 16);
+        p.units = cut ? (int)units : 0;
+        p.grid = ((cut ? units : B) + 7) / 8 * 8 * Hkv;
+        rows = cut ? (size_t)units * Hkv * R : 0;
+    } else {
+        p.min_tiles = 4;
+        int64_t want = (512 + groups - 1) / groups;
+        const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
+        want = want < most ? want : most;
+        p.nsplit = (int)(want > 1 ? want : 1);
+        p.grid = groups * p.nsplit;
+        rows = p.nsplit > 1 ? (size_t)groups / p.row_tiles * p.nsplit * R : 0;
+    }
     p.part_off = up(p.ml_off + 8 * rows);
-    p.ws_bytes = p.nsplit > 1 ? up(p.part_off + 4 * rows * p.dp) : kWsFixedBytes;
+    p.ws_bytes = rows ? up(p.part_off + 4 * rows * p.dp) : kWsFixedBytes;
     return p;
 }
 
@@ -301,14 +332,14 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
     if (check_attention("tree attention", RTOPK_F16, B, N, Hq, Hkv, D, 1.f) != RTOPK_OK || N > rtopk::kMaxTree ||
         table_ld < 1 || page < 1 || !mul_fits(table_ld, page, INT_MAX - 4096))
         return 0;
-    return rtopk::plan_attention(B, N, Hq, Hkv, D, table_ld * page).ws_bytes;
+    return attention_bytes(B, N, Hq, Hkv, D, table_ld * page);
 }
 
 size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hkv, int D)
 {
     if (check_attention("cross attention", RTOPK_F16, B, N, Hq, Hkv, D, 1.f) != RTOPK_OK || S < 1 || S > INT_MAX - 4096)
         return 0;
-    return rtopk::plan_attention(B, N, Hq, Hkv, D, S).ws_bytes;
+    return attention_bytes(B, N, Hq, Hkv, D, S);
 }
 
 int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, const void *v,
