@@ -23,7 +23,6 @@ struct TableArgs {
     int32_t *cu;                // [B + 1]
     int32_t *next;              // [1] or null
 };
-int64_t page_tables_blocks(int64_t cap);
 hipError_t launch_page_tables(const TableArgs &a, hipStream_t s);
 
 // Store of new keys and values; strides and counts in units of a load.
