@@ -56,15 +56,6 @@ template <> struct Elem<2> {
 // The keys of a row that counts no key come from here.
 __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
-// Workgroup w runs on XCD w mod 8; logical workgroup numbers give every XCD
-// one contiguous part of the grid, so that workgroups that read the same keys
-// share an L2.
-__device__ __forceinline__ int xcd_order(int w, int n)
-{
-    const int per = n / 8, rest = n % 8, x = w % 8;
-    return x * per + (x < rest ? x : rest) + w / 8;
-}
-
 // Keys of batch element b that any of its rows may see: [0, end), and where its
 // tree begins (tree: the nodes are at tree0 ... tree0 + size - 1).
 struct KeyRange {
@@ -144,12 +135,16 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
-    int w = xcd_order((int)blockIdx.x, (int)gridDim.x);
-    const int rt = w % a.row_tiles;
-    w /= a.row_tiles;
-    const int split = w % a.nsplit;
-    w /= a.nsplit;
-    const int hk = w % a.Hkv, b = w / a.Hkv;
+    // workgroup w runs on XCD w mod 8: the row tiles of one key head and split, which
+    // read the same keys, go to one XCD, the groups of them around all XCDs
+    // (their lengths differ)
+    const int xi = (int)blockIdx.x / 8, rt = xi % a.row_tiles;
+    int w = xi / a.row_tiles * 8 + (int)blockIdx.x % 8;
+    if (w >= a.B * a.Hkv * a.nsplit)
+        return;
+    const int hk = w % a.Hkv;
+    w /= a.Hkv;
+    const int split = w % a.nsplit, b = w / a.nsplit;
 
     const KeyRange kr = key_range<TREE>(a, b);
     const int R = kr.size * a.G, r0 = rt * 32 * WR;

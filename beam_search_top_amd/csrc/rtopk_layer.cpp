@@ -165,7 +165,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
         const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
         want = want < most ? want : most;
         p.nsplit = (int)(want > 1 ? want : 1);
-        p.grid = groups * p.nsplit;
+        p.grid = ((int64_t)B * Hkv * p.nsplit + 7) / 8 * 8 * p.row_tiles;
         rows = p.nsplit > 1 ? (size_t)groups / p.row_tiles * p.nsplit * R : 0;
     }
     p.part_off = up(p.ml_off + 8 * rows);
