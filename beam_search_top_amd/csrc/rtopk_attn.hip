@@ -19,8 +19,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
 // Global memory by its address space: a pointer that may be one of two others'
@@ -113,6 +111,31 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // unrounded ones, in float32.
 constexpr float kLazy = 8.f;
 
+// The A operands V^T of keys ROW ... ROW + 15 for DB blocks of 32 columns: per block
+// two transposing reads of four keys each. In one asm statement with its
+// wait: around the builtin the compiler waits for every direct-to-LDS load in
+// flight too, the next tile's among them, although the loop's barrier has
+// ordered the ones that matter.
+template <typename V8, int DB, int ROWB, int ROW>
+__device__ __forceinline__ void values_operand(V8 (&v)[DB], const int (&at)[DB], uint32_t base)
+{
+    constexpr int A = ROW * ROWB, B = (ROW + 8) * ROWB;
+#pragma unroll
+    for (int d = 0; d < DB; d += 2) {
+        u32x2 x0, x1, y0, y1;
+        asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+                     "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+                     "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+                     "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(x0), "=&v"(x1), "=&v"(y0), "=&v"(y1)
+                     : "v"(at[d] + base), "v"(at[d + 1] + base), "i"(A), "i"(B)
+                     : "memory");
+        v[d] = __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3));
+        v[d + 1] = __builtin_bit_cast(V8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3));
+    }
+}
+
 template <int DT, int DP, int WR, bool TREE>
 __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const AttnArgs a)
 {
@@ -131,7 +154,9 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
     __shared__ __align__(1024) uint8_t smem[4 * TILEB]; // K tiles 0 and 1, V tiles 0 and 1
     __shared__ uint64_t s_up[TREE ? kMaxTree * kWords : 1]; // ancestors of every node
     __shared__ int s_jump[TREE ? kMaxTree : 1];
-    __shared__ uint64_t s_odd[2]; // keys of the tile with infinities or NaN in their values
+    // keys with infinities or NaN in their values, a word per tile from the first that meets the tree on
+    constexpr int kOddTiles = kMaxTree / BN + 1;
+    __shared__ uint64_t s_odd[TREE ? kOddTiles : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
@@ -222,6 +247,9 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
             __syncthreads();
         }
     }
+    const int tree_tile = kr.tree0 / BN;
+    if (TREE && walk && tid < kOddTiles)
+        s_odd[tid] = 0; // a barrier of the loop comes before its use
     // whether this row's node sees key j of the tile at t0, one bit per key
     auto window = [&](int t0) -> uint64_t {
         const int off = t0 - kr.tree0; // node of the tile's first key
@@ -256,43 +284,62 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
             return a.table[(int64_t)b * a.ld + page_of(a.page, (uint32_t)j)];
         return a.key_mask ? a.key_mask[(int64_t)b * a.S + j] : 0;
     };
-    // starts the loads of tile t into buffer `buf`; the keys that count, one bit each
-    auto issue = [&](int t, int buf, int info) -> uint64_t {
+    struct Tile {
+        uint64_t oks; // the keys that count, one bit each
+        int64_t off;  // tree: byte offset of this lane's key, -1: does not count
+    };
+    auto place = [&](int t, int info) -> Tile {
         const int j = t * BN + lane;
-        bool ok = lane < BN && j < kr.end;
-        int64_t off = 0;
+        bool ok = lane < BN && t < t_end && j < kr.end;
+        Tile p{0, -1};
         if (TREE) {
             const int id = checked_page(info, a.num_pages);
             ok = ok && id >= 0;
             const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : 0));
-            off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
+            p.off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
         } else {
             ok = ok && info == 0;
         }
-        const uint64_t oks = __ballot(ok);
+        p.oks = __ballot(ok);
+        return p;
+    };
+    // starts the loads of tile t's keys (or values) into the buffer at `to`. Where
+    // every key counts and rows lie evenly (a load's on one page; 32-bit offsets), the wave
+    // computes a load's address once and the lanes only hold an offset.
+    const bool even = a.D == DP && (!TREE || a.page.d % 8 == 0) && a.ks[1] < (1 << 25) && a.vs[1] < (1 << 25);
+    auto load_tile = [&](const Tile &p, int t, const char *base, int64_t stride, bool values, uint8_t *to) {
+        if (even && p.oks == (BN == 64 ? ~0ull : (1ull << BN) - 1)) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int lr = (wave * NI + i) * RPL, r = lr + lrow;
+                const uint32_t off = lrow * (uint32_t)(2 * stride) + (lslot ^ (values ? fv(r) : r & FK)) * 16;
+                gchar *from = (gchar *)base;
+                if (TREE)
+                    from += (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(p.off >> 32), lr) << 32 |
+                                      (uint32_t)__builtin_amdgcn_readlane((int)p.off, lr));
+                else
+                    from += 2 * (int64_t)(t * BN + lr) * stride;
+                __builtin_amdgcn_global_load_lds((glb_void *)(from + off), (lds_void *)(to + lr * ROWB), 16, 0, 0);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int lr = (wave * NI + i) * RPL, r = lr + lrow;
-            const int ck = lslot ^ (r & FK), cv = lslot ^ fv(r);
-            const char *kp, *vp;
+            const int c = lslot ^ (values ? fv(r) : r & FK);
+            const char *from;
             bool in;
             if (TREE) {
-                const int64_t o = ((int64_t)__shfl((int)(off >> 32), r) << 32) | (uint32_t)__shfl((int)off, r);
+                const int64_t o = ((int64_t)__shfl((int)(p.off >> 32), r) << 32) | (uint32_t)__shfl((int)p.off, r);
                 in = o >= 0;
-                kp = kbase + o;
-                vp = vbase + o;
+                from = base + o;
             } else {
-                in = oks >> r & 1;
-                kp = kbase + 2 * (int64_t)(t * BN + r) * a.ks[1];
-                vp = vbase + 2 * (int64_t)(t * BN + r) * a.vs[1];
+                in = p.oks >> r & 1;
+                from = base + 2 * (int64_t)(t * BN + r) * stride;
             }
-            const char *z = reinterpret_cast<const char *>(g_zeros);
-            kp = in && ck * 8 < a.D ? kp + ck * 16 : z;
-            vp = in && cv * 8 < a.D ? vp + cv * 16 : z;
-            __builtin_amdgcn_global_load_lds((glb_void *)kp, (lds_void *)(smem + buf * TILEB + lr * ROWB), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((glb_void *)vp, (lds_void *)(smem + (2 + buf) * TILEB + lr * ROWB), 16, 0, 0);
+            from = in && c * 8 < a.D ? from + c * 16 : reinterpret_cast<const char *>(g_zeros);
+            __builtin_amdgcn_global_load_lds((glb_void *)from, (lds_void *)(to + lr * ROWB), 16, 0, 0);
         }
-        return oks;
     };
 
     f32x16 o[DB];
@@ -309,39 +356,52 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
     for (int d = 0; d < DB; ++d)
         vaddr[d] = vrow * ROWB + ((4 * d + vchunk) ^ fv(vrow)) * 16 + (lane & 1) * 8;
 
-    uint64_t oks = 0;
+    // X^T block k of the tile at ks
+    auto scores = [&](const uint8_t *ks, int k) -> f32x16 {
+        f32x16 x = {};
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+            const V8 kf = *reinterpret_cast<const V8 *>(ks + k * 32 * ROWB + kaddr + ((2 * c + half) ^ (col & FK)) * 16);
+            x = E::mfma(kf, q[c], x);
+        }
+        return x;
+    };
+    uint8_t *kbuf = smem, *vbuf = smem + 2 * TILEB;
+
+    // Keys run one tile ahead of values: the scores of tile t + 1 are multiplied
+    // while the weights of tile t are computed, so that a wave keeps the matrix
+    // cores and the vector unit busy at once.
+    Tile cur{0, -1}, nxt{0, -1};
+    f32x16 x0[KB], x1[KB]; // scores of this tile and the next, in turn
     int info = 0;
     if (t_begin < t_end) {
-        oks = issue(t_begin, 0, fetch(t_begin));
-        info = fetch(t_begin + 1);
-    }
-    for (int t = t_begin; t < t_end; ++t) {
-        const int buf = (t - t_begin) & 1;
-        // tile t is in LDS; every wave is done with the other buffer
-        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt(0)
+        cur = place(t_begin, fetch(t_begin));
+        load_tile(cur, t_begin, kbase, a.ks[1], false, kbuf);
+        nxt = place(t_begin + 1, fetch(t_begin + 1));
+        info = fetch(t_begin + 2);
         __syncthreads();
-        const uint64_t now = oks;
-        if (t + 1 < t_end) {
-            oks = issue(t + 1, buf ^ 1, info);
-            info = fetch(t + 2);
-        }
-        const uint8_t *ks = smem + buf * TILEB, *vs = smem + (2 + buf) * TILEB;
+        load_tile(nxt, t_begin + 1, kbase, a.ks[1], false, kbuf + TILEB);
+        load_tile(cur, t_begin, vbase, a.vs[1], true, vbuf);
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+            x0[k] = scores(kbuf, k);
+    }
+    auto step = [&](int t, auto buf_, f32x16 (&x)[KB], f32x16 (&y)[KB]) {
+        constexpr int buf = decltype(buf_)::value;
+        // keys t + 1 and values t are in LDS; every wave is done with keys t and values t - 1
+        __syncthreads();
+        const Tile far = place(t + 2, info);
+        if (t + 2 < t_end)
+            load_tile(far, t + 2, kbase, a.ks[1], false, kbuf + buf * TILEB);
+        if (t + 1 < t_end)
+            load_tile(nxt, t + 1, vbase, a.vs[1], true, vbuf + (buf ^ 1) * TILEB);
+        info = fetch(t + 3);
+        const uint8_t *ks = kbuf + (buf ^ 1) * TILEB, *vs = vbuf + buf * TILEB;
 
-        // ---- scores
-        f32x16 x[KB];
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            x[k] = f32x16{};
-#pragma unroll
-            for (int c = 0; c < DC; ++c) {
-                const V8 kf = *reinterpret_cast<const V8 *>(ks + k * 32 * ROWB + kaddr + ((2 * c + half) ^ (col & FK)) * 16);
-                x[k] = E::mfma(kf, q[c], x[k]);
-            }
-        }
         const bool in_tree = walk && (t + 1) * BN > kr.tree0;
         const uint64_t all = BN == 64 ? ~0ull : (1ull << BN) - 1;
-        uint64_t see = now;
-        const bool masked = now != all || in_tree;
+        uint64_t see = cur.oks;
+        const bool masked = see != all || in_tree;
         if (masked) {
             if (in_tree)
                 see &= window(t * BN);
@@ -352,13 +412,16 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
                 for (int i = 0; i < 16; ++i)
                     x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : -INFINITY;
         }
-        // ---- the running maximum
-        float mx = x[0][0];
+        // ---- the running maximum; scores of the next tile (the last tile's are of whatever
+        // lies there, and not used)
+        if constexpr (KB > 1)
+            y[0] = scores(ks, 0);
+        float mx = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                mx = fmaxf(mx, x[k][i]);
+            for (int i = 0; i < 16; i += 2)
+                mx = fmaxf(fmaxf(mx, x[k][i]), x[k][i + 1]);
         {
             const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
             mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
@@ -376,12 +439,12 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
         // ---- weights
         const float mu = m == -INFINITY ? 0.f : m;
         V8 p[KB][2];
+        y[KB - 1] = scores(ks, KB - 1);
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
+        for (int k = 0; k < KB; ++k)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 x[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][i], cs, -mu));
-        }
         if (masked && cs == 0.f) { // 0 * -inf is not -inf
             const uint64_t bits = see >> (4 * half);
 #pragma unroll
@@ -390,21 +453,19 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
                 for (int i = 0; i < 16; ++i)
                     x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : 0.f;
         }
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                l += x[k][i];
+                part[i % 4] += x[k][i];
                 p[k][i / 8][i % 8] = (T)x[k][i];
             }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
         // ---- a node's infinities and NaN must not reach the rows that do not
         // see it: they leave the tile, and are added afterwards where they belong
-        uint64_t odd = 0;
         if (TREE && in_tree) {
-            if (tid < 2)
-                s_odd[tid] = 0;
-            __syncthreads();
-            uint8_t *vw = smem + (2 + buf) * TILEB;
+            uint8_t *vw = vbuf + buf * TILEB;
             for (int u = tid; u < TILEB / 16; u += 64 * WR) {
                 u32x4 *at = reinterpret_cast<u32x4 *>(vw + u * 16);
                 u32x4 y = *at;
@@ -417,44 +478,66 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
                 }
                 if (any) {
                     *at = y;
-                    atomicOr((unsigned long long *)&s_odd[0], 1ull << (u / CH));
+                    atomicOr((unsigned long long *)&s_odd[t - tree_tile], 1ull << (u / CH));
                 }
             }
             __syncthreads();
-            odd = s_odd[0];
         }
-        // ---- outputs
+        // ---- outputs. The next product's operands are read before this one is
+        // multiplied, which hides most of the wait for them
+        const uint32_t vb = (uint32_t)(uintptr_t)(lds_void *)vs;
+        V8 vf[2][DB];
+        values_operand<V8, DB, ROWB, 0>(vf[0], vaddr, vb);
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int k = 0; k < KB; ++k)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint8_t *vp = vs + vaddr[d] + (32 * k + 16 * c) * ROWB;
-                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)vp);
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vp + 8 * ROWB));
-                    const V8 vf = __builtin_bit_cast(V8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                    o[d] = E::mfma(vf, p[k][c], o[d]);
-                }
-        while (TREE && odd) {
-            const int j = __ffsll((unsigned long long)odd) - 1;
-            odd &= odd - 1;
-            if (!(see >> j & 1))
-                continue;
-            const int pos = t * BN + j, pg = (int)page_of(a.page, (uint32_t)pos);
-            const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
-            const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+        for (int n = 0; n < 2 * KB; ++n) { // 16 keys each
+            if (n == 0)
+                values_operand<V8, DB, ROWB, 16>(vf[1], vaddr, vb);
+            if constexpr (KB > 1) {
+                if (n == 1)
+                    values_operand<V8, DB, ROWB, 32>(vf[0], vaddr, vb);
+                if (n == 2)
+                    values_operand<V8, DB, ROWB, 48>(vf[1], vaddr, vb);
+            }
 #pragma unroll
             for (int d = 0; d < DB; ++d)
+                o[d] = E::mfma(vf[n % 2][d], p[n / 2][n % 2], o[d]);
+        }
+        cur = nxt;
+        nxt = far;
+    };
+    int t = t_begin;
+    for (; t + 1 < t_end; t += 2) {
+        step(t, std::integral_constant<int, 0>{}, x0, x1);
+        step(t + 1, std::integral_constant<int, 1>{}, x1, x0);
+    }
+    if (t < t_end)
+        step(t, std::integral_constant<int, 0>{}, x0, x1);
+    // what left the tiles, for the rows that see it: the sum is infinite or NaN whatever the weight
+    if (TREE && walk) {
+        __syncthreads();
+        for (int w = 0; w < kOddTiles; ++w) {
+            uint64_t odd = s_odd[w];
+            const uint64_t see = odd ? window((tree_tile + w) * BN) : 0;
+            while (odd) {
+                const int j = __ffsll((unsigned long long)odd) - 1;
+                odd &= odd - 1;
+                if (!(see >> j & 1))
+                    continue;
+                const int pos = (tree_tile + w) * BN + j, pg = (int)page_of(a.page, (uint32_t)pos);
+                const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
+                const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-                    if (e < a.D) {
-                        const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
-                        if ((raw & E::kExp) == E::kExp)
-                            o[d][i] += (float)vr[e];
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                        if (e < a.D) {
+                            const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
+                            if ((raw & E::kExp) == E::kExp)
+                                o[d][i] += (float)vr[e];
+                        }
                     }
-                }
+            }
         }
     }
     {
