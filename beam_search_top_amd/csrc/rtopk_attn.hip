@@ -96,8 +96,9 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // The A operand V^T, four keys of one column per load, comes from the
 // row-major tile by transposing LDS reads.
 //
-// Keys and values come by direct-to-LDS loads, double-buffered: while a tile is
-// multiplied, the next one is in flight. A row of a tile is DP elements; its
+// Keys and values come by direct-to-LDS loads into rings of ST tiles: ST - 1 tiles
+// are in flight while one is multiplied, and the wait for the oldest leaves the
+// others in flight. A row of a tile is DP elements; its
 // 16-byte chunks are permuted by the row (slot = chunk ^ f(row)), which keeps
 // both kinds of reads free of bank conflicts. A key that no row may see (past
 // the end, masked out, on a page that does not exist) is loaded from a line of
@@ -110,6 +111,26 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // step per weight, as much as the output's own rounding. Their sum is of the
 // unrounded ones, in float32.
 constexpr float kLazy = 8.f;
+
+// Tiles in each ring: as many as the LDS of a CU holds for one workgroup of
+// eight waves, or two for each of two workgroups of four.
+constexpr int ring_tiles(int wr) { return wr == 8 ? 4 : 2; }
+
+// Wait until at most N of this wave's loads are in flight (all of them where
+// fewer than those were started), then meet the other waves. A direct-to-LDS
+// load counts as done once its data is in LDS. (__syncthreads would wait for
+// every load.)
+template <int N> __device__ __forceinline__ void ring_wait(bool full)
+{
+    static_assert(N >= 0 && N < 64, "vmcnt field");
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if (full)
+        __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+    else
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
 // The A operands V^T of keys ROW ... ROW + 15 for DB blocks of 32 columns: per block
 // two transposing reads of four keys each. In one asm statement with its
@@ -149,9 +170,10 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
     constexpr int RPL = 1024 / ROWB;                  // rows of one 1 KiB load of a wave
     constexpr int NI = BN / RPL / WR > 0 ? BN / RPL / WR : 1; // loads per wave and tensor
     static_assert(BN % (RPL * WR) == 0, "a tile is whole loads of every wave");
+    constexpr int ST = ring_tiles(WR);
     constexpr int FK = CH < 16 ? CH - 1 : 15;
     constexpr int kWords = kMaxTree / 64;
-    __shared__ __align__(1024) uint8_t smem[4 * TILEB]; // K tiles 0 and 1, V tiles 0 and 1
+    __shared__ __align__(1024) uint8_t smem[2 * ST * TILEB]; // a ring of K tiles, a ring of V tiles
     __shared__ uint64_t s_up[TREE ? kMaxTree * kWords : 1]; // ancestors of every node
     __shared__ int s_jump[TREE ? kMaxTree : 1];
     // keys with infinities or NaN in their values, a word per tile from the first that meets the tree on
@@ -248,8 +270,11 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
         }
     }
     const int tree_tile = kr.tree0 / BN;
-    if (TREE && walk && tid < kOddTiles)
-        s_odd[tid] = 0; // a barrier of the loop comes before its use
+    if (TREE && walk) {
+        if (tid < kOddTiles)
+            s_odd[tid] = 0;
+        __syncthreads();
+    }
     // whether this row's node sees key j of the tile at t0, one bit per key
     auto window = [&](int t0) -> uint64_t {
         const int off = t0 - kr.tree0; // node of the tile's first key
@@ -275,30 +300,54 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
     const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
     const int lrow = lane / CH, lslot = lane % CH;
     auto fv = [](int r) { return CH < 16 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; };
-    // what decides about key t0 + lane, read one tile ahead: its page, or its mask
-    auto fetch = [&](int t) -> int {
-        const int j = t * BN + lane;
-        if (lane >= BN || j >= kr.end)
-            return -1;
-        if (TREE)
-            return a.table[(int64_t)b * a.ld + page_of(a.page, (uint32_t)j)];
-        return a.key_mask ? a.key_mask[(int64_t)b * a.S + j] : 0;
+    // What decides about a key, its page or its mask, for a window of keys that
+    // is read ahead now and then: lane l holds the page id of page win + l, or
+    // the masks of keys win + 8 l ... + 7. The wait for it stays in the branch: a
+    // wait at the use would drain the loads in flight for every tile.
+    int win = 0, held = 0;
+    bool loaded = false;
+    auto refill = [&](int t) {
+        if (!TREE && !a.key_mask)
+            return;
+        const int j0 = t * BN, j1 = j0 + BN - 1 < kr.end - 1 ? j0 + BN - 1 : kr.end - 1;
+        if (TREE) {
+            const int pg = (int)page_of(a.page, (uint32_t)j1);
+            if (loaded && pg < win + 64)
+                return;
+            win = (int)page_of(a.page, (uint32_t)j0);
+            held = win + lane < a.ld ? a.table[(int64_t)b * a.ld + win + lane] : -1;
+        } else {
+            if (loaded && j1 < win + 512)
+                return;
+            win = j0;
+            const uint8_t *mp = a.key_mask + (int64_t)b * a.S + win + 8 * lane;
+            held = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                held |= (win + 8 * lane + e < a.S && mp[e] != 0) << e;
+        }
+        loaded = true;
+        asm volatile("" : "+v"(held));
     };
     struct Tile {
         uint64_t oks; // the keys that count, one bit each
         int64_t off;  // tree: byte offset of this lane's key, -1: does not count
     };
-    auto place = [&](int t, int info) -> Tile {
-        const int j = t * BN + lane;
-        bool ok = lane < BN && t < t_end && j < kr.end;
+    auto place = [&](int t) -> Tile {
         Tile p{0, -1};
+        if (t >= t_end)
+            return p;
+        refill(t);
+        const int j = t * BN + lane;
+        bool ok = lane < BN && j < kr.end;
         if (TREE) {
-            const int id = checked_page(info, a.num_pages);
+            const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : t * BN));
+            const int id = checked_page(__shfl(held, pg - win), a.num_pages);
             ok = ok && id >= 0;
-            const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : 0));
             p.off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
-        } else {
-            ok = ok && info == 0;
+        } else if (a.key_mask) {
+            const int w = t * BN + lane - win, out = __shfl(held, (w >> 3) & 63) >> (w & 7) & 1; // for every lane: none may be idle
+            ok = ok && !out;
         }
         p.oks = __ballot(ok);
         return p;
@@ -366,41 +415,48 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
         }
         return x;
     };
-    uint8_t *kbuf = smem, *vbuf = smem + 2 * TILEB;
+    uint8_t *kbuf = smem, *vbuf = smem + ST * TILEB;
 
     // Keys run one tile ahead of values: the scores of tile t + 1 are multiplied
     // while the weights of tile t are computed, so that a wave keeps the matrix
     // cores and the vector unit busy at once.
-    Tile cur{0, -1}, nxt{0, -1};
     f32x16 x0[KB], x1[KB]; // scores of this tile and the next, in turn
-    int info = 0;
+    uint64_t oks[ST + 1];  // of tiles t, t + 1, ...
+    Tile last{0, -1};      // the last tile whose keys are on their way
+#pragma unroll
+    for (int i = 0; i <= ST; ++i)
+        oks[i] = 0;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) { // keys 0; keys 1, values 0; keys 2, values 1; ...
+        const Tile p = place(t_begin + i);
+        oks[i] = p.oks;
+        if (t_begin + i < t_end)
+            load_tile(p, t_begin + i, kbase, a.ks[1], false, kbuf + i * TILEB);
+        if (i > 0 && t_begin + i - 1 < t_end)
+            load_tile(last, t_begin + i - 1, vbase, a.vs[1], true, vbuf + (i - 1) * TILEB);
+        last = p;
+    }
     if (t_begin < t_end) {
-        cur = place(t_begin, fetch(t_begin));
-        load_tile(cur, t_begin, kbase, a.ks[1], false, kbuf);
-        nxt = place(t_begin + 1, fetch(t_begin + 1));
-        info = fetch(t_begin + 2);
-        __syncthreads();
-        load_tile(nxt, t_begin + 1, kbase, a.ks[1], false, kbuf + TILEB);
-        load_tile(cur, t_begin, vbase, a.vs[1], true, vbuf);
+        ring_wait<2 * (ST - 1) * NI>(t_begin + ST <= t_end);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
             x0[k] = scores(kbuf, k);
     }
-    auto step = [&](int t, auto buf_, f32x16 (&x)[KB], f32x16 (&y)[KB]) {
-        constexpr int buf = decltype(buf_)::value;
+    auto step = [&](int t, f32x16 (&x)[KB], f32x16 (&y)[KB]) {
         // keys t + 1 and values t are in LDS; every wave is done with keys t and values t - 1
-        __syncthreads();
-        const Tile far = place(t + 2, info);
-        if (t + 2 < t_end)
-            load_tile(far, t + 2, kbase, a.ks[1], false, kbuf + buf * TILEB);
-        if (t + 1 < t_end)
-            load_tile(nxt, t + 1, vbase, a.vs[1], true, vbuf + (buf ^ 1) * TILEB);
-        info = fetch(t + 3);
-        const uint8_t *ks = kbuf + (buf ^ 1) * TILEB, *vs = vbuf + buf * TILEB;
+        const int at = (t - t_begin) & (ST - 1);
+        ring_wait<2 * (ST - 2) * NI>(t + ST <= t_end);
+        if (t + ST - 1 < t_end)
+            load_tile(last, t + ST - 1, vbase, a.vs[1], true, vbuf + ((at + ST - 1) & (ST - 1)) * TILEB);
+        last = place(t + ST);
+        if (t + ST < t_end)
+            load_tile(last, t + ST, kbase, a.ks[1], false, kbuf + at * TILEB);
+        oks[ST] = last.oks;
+        const uint8_t *ks = kbuf + ((at + 1) & (ST - 1)) * TILEB, *vs = vbuf + at * TILEB;
 
         const bool in_tree = walk && (t + 1) * BN > kr.tree0;
         const uint64_t all = BN == 64 ? ~0ull : (1ull << BN) - 1;
-        uint64_t see = cur.oks;
+        uint64_t see = oks[0];
         const bool masked = see != all || in_tree;
         if (masked) {
             if (in_tree)
@@ -465,10 +521,10 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
         // ---- a node's infinities and NaN must not reach the rows that do not
         // see it: they leave the tile, and are added afterwards where they belong
         if (TREE && in_tree) {
-            uint8_t *vw = vbuf + buf * TILEB;
+            uint8_t *vw = vbuf + at * TILEB;
             for (int u = tid; u < TILEB / 16; u += 64 * WR) {
-                u32x4 *at = reinterpret_cast<u32x4 *>(vw + u * 16);
-                u32x4 y = *at;
+                u32x4 *place = reinterpret_cast<u32x4 *>(vw + u * 16);
+                u32x4 y = *place;
                 bool any = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -477,7 +533,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
                     y[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
                 }
                 if (any) {
-                    *at = y;
+                    *place = y;
                     atomicOr((unsigned long long *)&s_odd[t - tree_tile], 1ull << (u / CH));
                 }
             }
@@ -502,16 +558,17 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
             for (int d = 0; d < DB; ++d)
                 o[d] = E::mfma(vf[n % 2][d], p[n / 2][n % 2], o[d]);
         }
-        cur = nxt;
-        nxt = far;
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+            oks[i] = oks[i + 1];
     };
     int t = t_begin;
     for (; t + 1 < t_end; t += 2) {
-        step(t, std::integral_constant<int, 0>{}, x0, x1);
-        step(t + 1, std::integral_constant<int, 1>{}, x1, x0);
+        step(t, x0, x1);
+        step(t + 1, x1, x0);
     }
     if (t < t_end)
-        step(t, std::integral_constant<int, 0>{}, x0, x1);
+        step(t, x0, x1);
     // what left the tiles, for the rows that see it: the sum is infinite or NaN whatever the weight
     if (TREE && walk) {
         __syncthreads();
@@ -1255,8 +1312,10 @@ template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, c
         hipLaunchKernelGGL((attn_tiles<DT, DP, 1, TREE>), grid, dim3(64), 0, s, a);
     else if (p.waves == 2)
         hipLaunchKernelGGL((attn_tiles<DT, DP, 2, TREE>), grid, dim3(128), 0, s, a);
-    else
+    else if (p.waves == 4 || DP > 128)
         hipLaunchKernelGGL((attn_tiles<DT, DP, 4, TREE>), grid, dim3(256), 0, s, a);
+    else if constexpr (DP <= 128)
+        hipLaunchKernelGGL((attn_tiles<DT, DP, 8, TREE>), grid, dim3(512), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.nsplit > 1) {
         const int64_t rows = (int64_t)a.B * a.N * a.Hq;

@@ -141,7 +141,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
     const int64_t R = (int64_t)N * (Hq / Hkv);
     p.few = p.dp <= 128 && R <= 32 && !wide ? (R <= 16 ? 1 : 2) : 0;
     p.bn = p.few || p.dp > 128 ? 32 : 64;
-    p.waves = p.few ? 4 : R <= 32 ? 1 : R <= 64 ? 2 : 4;
+    p.waves = p.few ? 4 : R <= 32 ? 1 : R <= 64 ? 2 : R <= 128 || p.dp > 128 ? 4 : 8;
     p.row_tiles = p.few ? 1 : (int)((R + 32 * p.waves - 1) / (32 * p.waves));
     const int64_t groups = (int64_t)B * Hkv * p.row_tiles, tiles = ((int64_t)S + p.bn - 1) / p.bn;
     const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -161,7 +161,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
         rows = cut ? (size_t)units * Hkv * R : 0;
     } else {
         p.min_tiles = 4;
-        int64_t want = (512 + groups - 1) / groups;
+        int64_t want = ((p.waves == 8 ? 256 : 512) + groups - 1) / groups; // a workgroup for every place
         const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
         want = want < most ? want : most;
         p.nsplit = (int)(want > 1 ? want : 1);
