@@ -158,7 +158,7 @@ __device__ __forceinline__ void values_operand(V8 (&v)[DB], const int (&at)[DB],
 }
 
 template <int DT, int DP, int WR, bool TREE>
-__global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const AttnArgs a)
+__global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tiles(const AttnArgs a)
 {
     typedef Elem<DT> E;
     typedef typename E::T T;
@@ -355,20 +355,24 @@ __global__ __launch_bounds__(64 * WR, DP > 128 ? 1 : 2) void attn_tiles(const At
     // starts the loads of tile t's keys (or values) into the buffer at `to`. Where
     // every key counts and rows lie evenly (a load's on one page; 32-bit offsets), the wave
     // computes a load's address once and the lanes only hold an offset.
-    const bool even = a.D == DP && (!TREE || a.page.d % 8 == 0) && a.ks[1] < (1 << 25) && a.vs[1] < (1 << 25);
+    const bool even = (!TREE || a.page.d % 8 == 0) && a.ks[1] < (1 << 25) && a.vs[1] < (1 << 25);
     auto load_tile = [&](const Tile &p, int t, const char *base, int64_t stride, bool values, uint8_t *to) {
         if (even && p.oks == (BN == 64 ? ~0ull : (1ull << BN) - 1)) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int lr = (wave * NI + i) * RPL, r = lr + lrow;
-                const uint32_t off = lrow * (uint32_t)(2 * stride) + (lslot ^ (values ? fv(r) : r & FK)) * 16;
+                const int c = lslot ^ (values ? fv(r) : r & FK);
+                const uint32_t off = lrow * (uint32_t)(2 * stride) + c * 16;
                 gchar *from = (gchar *)base;
                 if (TREE)
                     from += (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(p.off >> 32), lr) << 32 |
                                       (uint32_t)__builtin_amdgcn_readlane((int)p.off, lr));
                 else
                     from += 2 * (int64_t)(t * BN + lr) * stride;
-                __builtin_amdgcn_global_load_lds((glb_void *)(from + off), (lds_void *)(to + lr * ROWB), 16, 0, 0);
+                from += off;
+                if (a.D < DP)
+                    from = c * 8 < a.D ? from : (gchar *)g_zeros;
+                __builtin_amdgcn_global_load_lds((glb_void *)from, (lds_void *)(to + lr * ROWB), 16, 0, 0);
             }
             return;
         }

@@ -487,10 +487,24 @@ def _strides(t, name):
     return _host_strides(st[:-1])
 
 
+_torch = None  # the module, once one of the functions below has run (an import per call costs a launch's time)
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _DTYPES.update({torch.float32: RTOPK_F32, torch.float16: RTOPK_F16, torch.bfloat16: RTOPK_BF16})
+    return _torch
+
+
+_DTYPES = {}
+
+
 def _ints(t, shape, dev, name):
     """A contiguous int32 device tensor of this shape."""
-    import torch
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
+    if t.dtype is not _torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
         _on_device(t, dev, name)
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
     return t.data_ptr()
@@ -498,7 +512,7 @@ def _ints(t, shape, dev, name):
 
 def _enqueue(dev, fn, *args):
     """fn(*args, stream) on dev's current stream, with dev the current device."""
-    import torch
+    torch = _torch
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             st = fn(*args, torch.cuda.current_stream().cuda_stream)
@@ -506,6 +520,10 @@ def _enqueue(dev, fn, *args):
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != RTOPK_OK:
         raise RtopkError(st, rtopk_last_error())
+
+
+def _code(t):
+    return _DTYPES[t.dtype] if t.dtype in _DTYPES else dtype_code(t)
 
 
 def page_tables(cache_lens, new_lens, page, free_pages, table, num_pages, free_head=None, tokens=None, rows=None,
@@ -517,7 +535,7 @@ def page_tables(cache_lens, new_lens, page, free_pages, table, num_pages, free_h
     [tokens], or laid out as [B, rows]; ``out`` may supply the four results.
     Returns (slots, positions, cu_new [B + 1], free_next [1]), all int32.
     """
-    import torch
+    torch = _get_torch()
     dev = table.device
     if not table.is_cuda or table.dim() != 2:
         raise ValueError("table must be a [B, ld] device tensor")
@@ -571,6 +589,7 @@ def cache_store(k, v, slots, k_cache, v_cache):
     are the tokens), slots int32 of the leading shape (a slot outside the cache
     skips its token), k_cache, v_cache [pages, page, Hkv, D]. Returns (k_cache, v_cache).
     """
+    _get_torch()
     dev = k.device
     if not k.is_cuda:
         raise ValueError("k must be a device tensor")
@@ -584,7 +603,7 @@ def cache_store(k, v, slots, k_cache, v_cache):
     pages, page, Hkv, D = _cache(k_cache, v_cache, k.dtype, dev)
     if k.shape[1:] != (Hkv, D):
         raise ValueError("k and v must have the cache's heads")
-    _enqueue(dev, load().rtopk_cache_store, k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), dtype_code(k),
+    _enqueue(dev, load().rtopk_cache_store, k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), _code(k),
              _ints(slots, slots.shape, dev, "slots"), k.shape[0], Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(),
              _strides(k_cache, "k_cache"), pages, page)
     return k_cache, v_cache
@@ -592,18 +611,17 @@ def cache_store(k, v, slots, k_cache, v_cache):
 
 def _attention_args(q, Hkv, scale, out, lse, workspace, dev):
     """Checks what both attentions share; returns the scale, out and the addresses of lse and the workspace."""
-    import torch
-    B, N, Hq, D = q.shape
+    B, N, Hq, D = shape = q.shape
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
+        out = _torch.empty(shape, dtype=q.dtype, device=dev)
+    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
         _on_device(out, dev, "out")
         raise ValueError("out must be a contiguous tensor of q's shape and type")
     lp = None
     if lse is not None:
-        if lse.shape != q.shape[:3] or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        if lse.shape != shape[:3] or lse.dtype is not _torch.float32 or not lse.is_contiguous() or lse.device != dev:
             _on_device(lse, dev, "lse")
             raise ValueError("lse must be a contiguous float32 [B, N, Hq] tensor")
         lp = lse.data_ptr()
@@ -626,6 +644,7 @@ def tree_attention(q, k_cache, v_cache, table, cache_lens, parents=None, sizes=N
     rtopk_tree_attention_workspace_bytes(...) bytes) is needed under graph
     capture. Returns (out, lse); lse None unless supplied.
     """
+    _get_torch()
     dev = q.device
     if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")
@@ -636,7 +655,7 @@ def tree_attention(q, k_cache, v_cache, table, cache_lens, parents=None, sizes=N
     ld = table.shape[1]
     scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
     _enqueue(dev, load().rtopk_tree_attention, q.data_ptr(), _strides(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
-             _strides(k_cache, "k_cache"), dtype_code(q), _ints(table, (B, ld), dev, "table"), ld, pages, page,
+             _strides(k_cache, "k_cache"), _code(q), _ints(table, (B, ld), dev, "table"), ld, pages, page,
              _ints(cache_lens, (B,), dev, "cache_lens"), None if parents is None else _ints(parents, (B, N), dev, "parents"),
              None if sizes is None else _ints(sizes, (B,), dev, "sizes"), B, N, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
     return out, lse
@@ -650,7 +669,7 @@ def cross_attention(q, k, v, lens=None, key_mask=None, scale=None, out=None, lse
     key_mask [B, S] uint8/bool, nonzero = left out; the rest as
     tree_attention. Returns (out, lse).
     """
-    import torch
+    torch = _get_torch()
     dev = q.device
     if not q.is_cuda or q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and k, v [B, S, Hkv, D]")
@@ -671,7 +690,7 @@ def cross_attention(q, k, v, lens=None, key_mask=None, scale=None, out=None, lse
         mp = key_mask.data_ptr()
     scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
     _enqueue(dev, load().rtopk_cross_attention, q.data_ptr(), _strides(q, "q"), k.data_ptr(), _strides(k, "k"),
-             v.data_ptr(), _strides(v, "v"), dtype_code(q), None if lens is None else _ints(lens, (B,), dev, "lens"), mp,
+             v.data_ptr(), _strides(v, "v"), _code(q), None if lens is None else _ints(lens, (B,), dev, "lens"), mp,
              B, N, S, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
     return out, lse
 
