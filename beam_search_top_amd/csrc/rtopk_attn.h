@@ -42,6 +42,7 @@ hipError_t launch_cache_store(StoreArgs a, int unit_bytes, hipStream_t s);
 constexpr int kMaxTree = 256;   // nodes of a tree
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxParts = 64;   // shares of a batch element in attn_few
+constexpr int kMaxShareBatch = 256; // batch elements whose lengths a wave of attn_few sums
 
 // Attention of N query rows per batch element over its keys (rtopk_attn.hip).
 struct AttnArgs {

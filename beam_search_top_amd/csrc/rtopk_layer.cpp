@@ -126,47 +126,54 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
 
 } // namespace
 
-#ifndef FEW_MIN
-#define FEW_MIN 4
-#define FEW_S64 1024
-#define FEW_S128 512
-#define FEW_MULT 0
-#endif
 namespace rtopk {
 
 AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
 {
     AttnPlan p{};
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    const int64_t R = (int64_t)N * (Hq / Hkv);
-    p.few = p.dp <= 128 && R <= 32 && !wide ? (R <= 16 ? 1 : 2) : 0;
-    p.bn = p.few || p.dp > 128 ? 32 : 64;
-    p.waves = p.few ? 4 : R <= 32 ? 1 : R <= 64 ? 2 : R <= 128 || p.dp > 128 ? 4 : 8;
-    p.row_tiles = p.few ? 1 : (int)((R + 32 * p.waves - 1) / (32 * p.waves));
-    const int64_t groups = (int64_t)B * Hkv * p.row_tiles, tiles = ((int64_t)S + p.bn - 1) / p.bn;
+    const int64_t R = (int64_t)N * (Hq / Hkv); // query rows that read the same keys
     const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     p.nsplit = 1;
     p.ml_off = up(kWsFixedBytes);
     size_t rows = 0; // rows of partial outputs
+    // Up to 32 rows the call is bound by reading, which attn_few is made for; with
+    // more, attn_tiles shares each key among 32 rows of every wave (8 rows x 4 heads
+    // over 4 x 30001 keys: attn_tiles 120 us, attn_few 90 us).
+    p.few = p.dp <= 128 && R <= 32 && !wide ? (R <= 16 ? 1 : 2) : 0;
     if (p.few) {
-        // Shares for every place on the GPU (3 workgroups per CU, 4 at D <= 64), and
-        // several per batch element when there are many of those
-        p.min_tiles = FEW_MIN;
-        int64_t units = ((p.dp == 64 ? FEW_S64 : FEW_S128) + Hkv - 1) / Hkv;
-        units = units > (FEW_MULT > 0 ? FEW_MULT : 2) * B ? units : (FEW_MULT > 0 ? FEW_MULT : 2) * B;
-        const bool cut = tiles > p.min_tiles && (FEW_MULT > 0 || (int64_t)B * Hkv < (p.dp == 64 ? FEW_S64 : FEW_S128)) && B <= 256 && (int64_t)B * Hkv <= kTicketCap && (int64_t)B * tiles <= (1 << 30) &&
-                         units <= (1 << 16);
+        // The keys are cut when the batch elements' key heads alone do not fill the
+        // GPU (2 workgroups per CU hold enough loads in flight at D = 128, 4 at D = 64:
+        // with 3 and 8 the call above takes 107 and 110 us). 128 x 16 of them are not
+        // cut: 34 us, cut in two or more 44 us, for the ends of every share cost more
+        // than the balance gains.
+        p.bn = 32;
+        p.waves = 4;
+        p.row_tiles = 1;
+        p.min_tiles = 4;
+        const int64_t places = p.dp == 64 ? 1024 : 512, tiles = ((int64_t)S + p.bn - 1) / p.bn;
+        int64_t units = (places + Hkv - 1) / Hkv;
+        units = units > 2 * (int64_t)B ? units : 2 * (int64_t)B;
+        const bool cut = tiles > p.min_tiles && (int64_t)B * Hkv < places && B <= kMaxShareBatch &&
+                         (int64_t)B * tiles <= (1 << 30);
         p.units = cut ? (int)units : 0;
         p.grid = ((cut ? units : B) + 7) / 8 * 8 * Hkv;
         rows = cut ? (size_t)units * Hkv * R : 0;
     } else {
+        // 32 rows per wave; from 129 rows on a workgroup of eight waves, whose rings fill a CU's
+        // LDS, else two workgroups of up to four per CU. Keys are cut, evenly per batch
+        // element, until every place has a workgroup.
+        p.waves = R <= 32 ? 1 : R <= 64 ? 2 : R <= 128 || p.dp > 128 ? 4 : 8;
+        p.bn = p.dp > 128 ? 32 : 64;
+        p.row_tiles = (int)((R + 32 * p.waves - 1) / (32 * p.waves));
         p.min_tiles = 4;
-        int64_t want = ((p.waves == 8 ? 256 : 512) + groups - 1) / groups; // a workgroup for every place
-        const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
+        const int64_t groups = (int64_t)B * Hkv * p.row_tiles, places = p.waves == 8 ? 256 : 512;
+        const int64_t tiles = ((int64_t)S + p.bn - 1) / p.bn, most = (tiles + p.min_tiles - 1) / p.min_tiles;
+        int64_t want = (places + groups - 1) / groups;
         want = want < most ? want : most;
         p.nsplit = (int)(want > 1 ? want : 1);
         p.grid = ((int64_t)B * Hkv * p.nsplit + 7) / 8 * 8 * p.row_tiles;
-        rows = p.nsplit > 1 ? (size_t)groups / p.row_tiles * p.nsplit * R : 0;
+        rows = p.nsplit > 1 ? (size_t)B * Hkv * p.nsplit * R : 0;
     }
     p.part_off = up(p.ml_off + 8 * rows);
     p.ws_bytes = rows ? up(p.part_off + 4 * rows * p.dp) : kWsFixedBytes;
