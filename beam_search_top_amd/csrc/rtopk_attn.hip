@@ -210,8 +210,10 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
     const int node = live ? row / a.G : 0, head = hk * a.G + (live ? row - node * a.G : 0);
     V8 q[DC];
     {
-        const T *qp = static_cast<const T *>(a.q) + b * a.qs[0] + node * a.qs[1] + head * a.qs[2];
+        // the sign is applied here, before the rings start: a wait for the rows later
+        // would be one for the rings too
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u; // scores by |scale|: the maximum stays a maximum
+        const T *qp = static_cast<const T *>(a.q) + b * a.qs[0] + node * a.qs[1] + head * a.qs[2];
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
             const int d = 16 * c + 8 * half;
@@ -910,16 +912,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             }
         }
     };
-    int t = t_begin + wave;
-    Step now = place(t, fetch(t));
-    load_keys(now, t);
-    int info = fetch(t + kFewWaves);
-    load_values(now, t);
-
     // ---- this lane's query rows
     u32x4 q[NB][DC];
     int node[NB], head[NB];
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int row = 16 * n + col;
@@ -933,8 +928,21 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             u32x4 x = {0, 0, 0, 0};
             if (live && e < a.D)
                 x = *(gu32x4 *)(qp + 2 * e);
-            q[n][c] = x ^ flip;
+            q[n][c] = x;
         }
+    }
+    int t = t_begin + wave;
+    Step now = place(t, fetch(t));
+    load_keys(now, t);
+    int info = fetch(t + kFewWaves);
+    load_values(now, t);
+
+    if (a.scale < 0.f) { // scores by |scale|: the maximum stays a maximum
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < DC; ++c)
+                q[n][c] ^= 0x80008000u;
     }
     const float cs = fabsf(a.scale) * kLog2e;
     // the nodes that each of its rows sees (at most 32 nodes: R <= 16 NB)
