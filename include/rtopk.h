@@ -469,8 +469,9 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
  *   out, lse   as rtopk_tree_attention (N any, B*N*Hq*D < 2^31)
  * Workspace: keys are split over workgroups when there are few rows, and the
  * parts are joined in a fixed order. workspace NULL uses the library-owned
- * workspace of `stream` (as rtopk_beam_step); a call that a graph captures is
- * then refused (RTOPK_EINVAL) if it needs one. A caller's workspace holds
+ * workspace of `stream` (as rtopk_beam_step; calls that use one stream's come
+ * from one thread at a time); a call that a graph captures is then refused
+ * (RTOPK_EINVAL) if it needs one. A caller's workspace holds
  * ws_bytes >= rtopk_cross_attention_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use (it may be one of
  * rtopk_beam_step_ws); calls sharing it must be ordered, so graphs that may

@@ -380,6 +380,48 @@ def test_tree_far_offsets():
     assert torch.equal(kc.view(-1, Hkv, D)[far.long()], k) and torch.equal(vc.view(-1, Hkv, D)[far.long()], k)
 
 
+# ------------------------------------------------------------------ many batch elements, long and far keys
+@pytest.mark.parametrize("B,N,S,Hkv,D", [(70, 2, 700, 1, 64), (256, 1, 300, 2, 128), (257, 1, 300, 1, 64), (130, 20, 400, 1, 128)])
+def test_cross_many_batch_elements(B, N, S, Hkv, D):
+    # shares of keys across up to 256 lengths, empty and full ones among them; more than that one share each
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, S + 1, B)
+    lens[::9] = 0
+    lens[3::17] = S
+    print(f"[cross many] B={B} N={N} S={S}", flush=True)
+    _cross(B, N, S, Hkv, Hkv, D, F16, seed=B, lens=lens.tolist())
+
+
+@pytest.mark.parametrize("B,N", [(65, 1), (200, 2), (40, 60)])
+def test_tree_many_requests(B, N):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 900, B)
+    sizes = rng.integers(0, N + 1, B)
+    lens[::7] = 0
+    print(f"[tree many] B={B} N={N}", flush=True)
+    _tree(_tree_inputs(B, N, 2, 1, 64, 16, lens.tolist(), BF16, seed=B, sizes=sizes.tolist()), f"many B={B}")
+
+
+@pytest.mark.parametrize("N,D", [(1, 64), (20, 128), (70, 64)])
+def test_cross_long(N, D):
+    # more shares than one batch element may have
+    print(f"[cross long] N={N} D={D}", flush=True)
+    _cross(1, N, 70001, 1, 1, D, BF16, seed=N, lens=[69990])
+
+
+@pytest.mark.parametrize("N", [2, 40])
+def test_cross_rows_far_apart(N):
+    # rows of keys 2^25 elements apart, in a buffer of more than 2^31 bytes
+    S, D, far = 35, 64, 1 << 25
+    g = _gen(N)
+    buf = torch.zeros(far * S, dtype=F16, device=DEV)
+    k = torch.as_strided(buf, (1, S, 1, D), (0, far, D, 1), 0)
+    v = torch.as_strided(buf, (1, S, 1, D), (0, far, D, 1), 128)
+    k.copy_(_rnd(g, 1, S, 1, D))
+    v.copy_(_rnd(g, 1, S, 1, D))
+    _cross(1, N, S, 2, 1, D, F16, seed=1, k=k, v=v)
+
+
 # ------------------------------------------------------------------ calls as programs make them
 def test_same_bits_every_time():
     c = _tree_inputs(2, 6, 8, 2, 128, 16, [3000, 41], BF16, seed=1)
