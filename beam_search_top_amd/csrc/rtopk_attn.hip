@@ -51,6 +51,16 @@ template <> struct Elem<2> {
     }
 };
 
+// Row swizzles of tiles whose rows are CH 16-byte chunks: chunk c of row r is at
+// slot c ^ f(r). LDS serves 256 bytes at a time: of keys 16 rows at one chunk
+// (fk), of values four rows at four neighbouring chunks (fv); both fall on
+// different banks then.
+template <int CH> __device__ __forceinline__ constexpr int fk(int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; }
+template <int CH> __device__ __forceinline__ constexpr int fv(int r)
+{
+    return CH == 8 ? (r & 2) << 1 | (r >> 1 & 2) : (r & 3) << 2 | (r >> 1 & 2);
+}
+
 // The keys of a row that counts no key come from here.
 __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
@@ -116,18 +126,19 @@ constexpr float kLazy = 8.f;
 // eight waves, or two for each of two workgroups of four.
 constexpr int ring_tiles(int wr) { return wr == 8 ? 4 : 2; }
 
-// Wait until at most N of this wave's loads are in flight (all of them where
-// fewer than those were started), then meet the other waves. A direct-to-LDS
-// load counts as done once its data is in LDS. (__syncthreads would wait for
-// every load.)
+// Wait until at most N of this wave's loads are in flight (none, where fewer
+// than those were started) and its LDS reads are done, then meet the other
+// waves: what the older loads brought can be read, and what was read can be
+// overwritten. A direct-to-LDS load counts as done once its data is in LDS.
+// (__syncthreads would wait for every load.)
 template <int N> __device__ __forceinline__ void ring_wait(bool full)
 {
     static_assert(N >= 0 && N < 64, "vmcnt field");
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     if (full)
-        __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+        __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14)); // vmcnt(N) lgkmcnt(0)
     else
-        __builtin_amdgcn_s_waitcnt(0x0f70);
+        __builtin_amdgcn_s_waitcnt(0x0070); // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
@@ -171,7 +182,6 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
     constexpr int NI = BN / RPL / WR > 0 ? BN / RPL / WR : 1; // loads per wave and tensor
     static_assert(BN % (RPL * WR) == 0, "a tile is whole loads of every wave");
     constexpr int ST = ring_tiles(WR);
-    constexpr int FK = CH < 16 ? CH - 1 : 15;
     constexpr int kWords = kMaxTree / 64;
     __shared__ __align__(1024) uint8_t smem[2 * ST * TILEB]; // a ring of K tiles, a ring of V tiles
     __shared__ uint64_t s_up[TREE ? kMaxTree * kWords : 1]; // ancestors of every node
@@ -301,7 +311,6 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
     const char *kbase = static_cast<const char *>(a.k) + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
     const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
     const int lrow = lane / CH, lslot = lane % CH;
-    auto fv = [](int r) { return CH < 16 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; };
     // What decides about a key, its page or its mask, for a window of keys that
     // is read ahead now and then: lane l holds the page id of page win + l, or
     // the masks of keys win + 8 l ... + 7. The wait for it stays in the branch: a
@@ -363,7 +372,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int lr = (wave * NI + i) * RPL, r = lr + lrow;
-                const int c = lslot ^ (values ? fv(r) : r & FK);
+                const int c = lslot ^ (values ? fv<CH>(r) : fk<CH>(r));
                 const uint32_t off = lrow * (uint32_t)(2 * stride) + c * 16;
                 gchar *from = (gchar *)base;
                 if (TREE)
@@ -381,7 +390,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int lr = (wave * NI + i) * RPL, r = lr + lrow;
-            const int c = lslot ^ (values ? fv(r) : r & FK);
+            const int c = lslot ^ (values ? fv<CH>(r) : fk<CH>(r));
             const char *from;
             bool in;
             if (TREE) {
@@ -409,14 +418,14 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
     int vaddr[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-        vaddr[d] = vrow * ROWB + ((4 * d + vchunk) ^ fv(vrow)) * 16 + (lane & 1) * 8;
+        vaddr[d] = vrow * ROWB + ((4 * d + vchunk) ^ fv<CH>(vrow)) * 16 + (lane & 1) * 8;
 
     // X^T block k of the tile at ks
     auto scores = [&](const uint8_t *ks, int k) -> f32x16 {
         f32x16 x = {};
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
-            const V8 kf = *reinterpret_cast<const V8 *>(ks + k * 32 * ROWB + kaddr + ((2 * c + half) ^ (col & FK)) * 16);
+            const V8 kf = *reinterpret_cast<const V8 *>(ks + k * 32 * ROWB + kaddr + ((2 * c + half) ^ fk<CH>(col)) * 16);
             x = E::mfma(kf, q[c], x);
         }
         return x;
@@ -791,7 +800,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
     typedef typename E::T T;
     constexpr int VE = DP / 16, DC = DP / 32, VW = VE / 2; // columns per lane, products per score, value dwords
     constexpr int ROWB = DP * 2, CH = DP / 8, RPL = 1024 / ROWB, NK = kFewStep / RPL; // a 1 KiB load is RPL rows
-    constexpr int FK = CH < 16 ? CH - 1 : 15;
     constexpr int PITCH = DP + 4;
     constexpr int KEYS = kFewWaves * kFewStep * ROWB, OUTS = kFewWaves * 16 * PITCH * 4;
     // the waves' keys; after the loop their outputs, a block of 16 rows at a time
@@ -988,7 +996,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int r = i * RPL + lrow;
-            *reinterpret_cast<u32x4 *>(mine + r * ROWB + (lchunk ^ (r & FK)) * 16) = kq[i];
+            *reinterpret_cast<u32x4 *>(mine + r * ROWB + (lchunk ^ fk<CH>(r)) * 16) = kq[i];
         }
         const Step next = place(t + kFewWaves, info);
         load_keys(next, t + kFewWaves);
@@ -1004,7 +1012,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             u32x4 kf[DC];
 #pragma unroll
             for (int c = 0; c < DC; ++c)
-                kf[c] = *reinterpret_cast<const u32x4 *>(mine + r * ROWB + ((4 * c + grp) ^ (r & FK)) * 16);
+                kf[c] = *reinterpret_cast<const u32x4 *>(mine + r * ROWB + ((4 * c + grp) ^ fk<CH>(r)) * 16);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 x[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
