@@ -63,6 +63,7 @@ struct AttnArgs {
     float *lse;                // [B][N][Hq] or null
     // the split over workgroups (plan_attention)
     int row_tiles, nsplit, min_tiles;
+    int longest_first;         // attn_tiles: batch elements in the order of their lengths (B <= 64)
     int units;                 // attn_few: shares of all batch elements at most, 0 = one each
     float *part;               // [B][Hkv][nsplit][N * G][dp] (attn_few: [units][Hkv][N * G][dp]) unnormalised outputs
     float *ml;                 // the same with [2] for [dp]: their maxima (base 2) and sums
@@ -73,7 +74,7 @@ struct AttnArgs {
 // by attn_few), tiles of `bn` keys, heads padded to `dp` elements, keys in at
 // most `nsplit` parts of at least min_tiles tiles (attn_few: in `units` shares).
 struct AttnPlan {
-    int few, dp, bn, waves, row_tiles, nsplit, min_tiles, units;
+    int few, dp, bn, waves, row_tiles, nsplit, min_tiles, units, longest_first;
     int64_t grid;
     size_t ml_off, part_off, ws_bytes; // workspace behind the fixed region
 };

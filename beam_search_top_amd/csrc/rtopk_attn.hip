@@ -201,7 +201,23 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
         return;
     const int hk = w % a.Hkv;
     w /= a.Hkv;
-    const int split = w % a.nsplit, b = w / a.nsplit;
+    const int split = w % a.nsplit;
+    int b = w / a.nsplit;
+    if (a.longest_first) {
+        // workgroups start in rounds: the batch element with the b-th most keys comes b-th, so
+        // that the last rounds are short ones (B <= 64: a lane per batch element)
+        int keys = -1;
+        if (lane < a.B) {
+            const KeyRange r = key_range<TREE>(a, lane);
+            keys = r.size > 0 ? r.end : 0;
+        }
+        int rank = lane < a.B ? 0 : 64;
+        for (int i = 0; i < a.B; ++i) {
+            const int other = __builtin_amdgcn_readlane(keys, i);
+            rank += other > keys || (other == keys && i < lane);
+        }
+        b = __ffsll((unsigned long long)__ballot(rank == b)) - 1;
+    }
 
     const KeyRange kr = key_range<TREE>(a, b);
     const int R = kr.size * a.G, r0 = rt * 32 * WR;

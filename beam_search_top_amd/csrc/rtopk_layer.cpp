@@ -110,6 +110,7 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
     a.nsplit = p.nsplit;
     a.min_tiles = p.min_tiles;
     a.units = p.units;
+    a.longest_first = p.longest_first && a.lens;
     const auto go = [&](void *ws) {
         a.ml = ws ? (float *)((uint8_t *)ws + p.ml_off) : nullptr;
         a.part = ws ? (float *)((uint8_t *)ws + p.part_off) : nullptr;
@@ -174,6 +175,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
         p.nsplit = (int)(want > 1 ? want : 1);
         p.grid = ((int64_t)B * Hkv * p.nsplit + 7) / 8 * 8 * p.row_tiles;
         rows = p.nsplit > 1 ? (size_t)B * Hkv * p.nsplit * R : 0;
+        p.longest_first = B > 1 && B <= 64 && groups > places;
     }
     p.part_off = up(p.ml_off + 8 * rows);
     p.ws_bytes = rows ? up(p.part_off + 4 * rows * p.dp) : kWsFixedBytes;

@@ -392,6 +392,19 @@ def test_cross_many_batch_elements(B, N, S, Hkv, D):
     _cross(B, N, S, Hkv, Hkv, D, F16, seed=B, lens=lens.tolist())
 
 
+def test_more_workgroups_than_places():
+    # they start longest first; equal, empty and full lengths among them
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 131, 40)
+    lens[::8] = 0
+    lens[1::8] = 130
+    lens[2::8] = 77
+    _cross(40, 260, 130, 4, 4, 64, F16, seed=4, lens=lens.tolist())
+    sizes = rng.integers(0, 71, 64)
+    c = _tree_inputs(64, 70, 24, 12, 64, 16, rng.integers(0, 90, 64).tolist(), BF16, seed=5, sizes=sizes.tolist())
+    _tree(c, "longest first")
+
+
 @pytest.mark.parametrize("B,N", [(65, 1), (200, 2), (40, 60)])
 def test_tree_many_requests(B, N):
     rng = np.random.default_rng(B)
