@@ -503,21 +503,21 @@ _DTYPES = {}
 
 
 def _ints(t, shape, dev, name):
-    """A contiguous int32 device tensor of this shape."""
-    if t.dtype is not _torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
-        _on_device(t, dev, name)
+    """The address of a contiguous int32 tensor of this shape on device number `dev`."""
+    if t.dtype is not _torch.int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _on_device(t, _torch.device("cuda", dev), name)
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
     return t.data_ptr()
 
 
 def _enqueue(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev the current device."""
-    torch = _torch
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    """fn(*args, stream) on the current stream of device number `dev`, with it the current device."""
+    cuda = _torch._C
+    if dev != cuda._cuda_getDevice():
+        with _torch.cuda.device(dev):
+            st = fn(*args, cuda._cuda_getCurrentRawStream(dev))
     else:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        st = fn(*args, cuda._cuda_getCurrentRawStream(dev))
     if st != RTOPK_OK:
         raise RtopkError(st, rtopk_last_error())
 
@@ -536,9 +536,9 @@ def page_tables(cache_lens, new_lens, page, free_pages, table, num_pages, free_h
     Returns (slots, positions, cu_new [B + 1], free_next [1]), all int32.
     """
     torch = _get_torch()
-    dev = table.device
     if not table.is_cuda or table.dim() != 2:
         raise ValueError("table must be a [B, ld] device tensor")
+    dev = table.get_device()
     B, ld = table.shape
     if out is not None:
         if len(out) != 4:
@@ -553,10 +553,10 @@ def page_tables(cache_lens, new_lens, page, free_pages, table, num_pages, free_h
         if (tokens is None) == (rows is None):
             raise ValueError("give one of tokens (packed slots) and rows (slots per request)")
         shape = torch.Size((tokens,) if rows is None else (B, rows))
-        slots = torch.empty(shape, dtype=torch.int32, device=dev)
+        slots = torch.empty(shape, dtype=torch.int32, device=table.device)
         positions = torch.empty_like(slots)
-        cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        nxt = torch.empty(1, dtype=torch.int32, device=dev)
+        cu = torch.empty(B + 1, dtype=torch.int32, device=table.device)
+        nxt = torch.empty(1, dtype=torch.int32, device=table.device)
     n = slots.numel()
     if n == 0 or len(shape) == 2 and shape[1] == 0:
         raise ValueError("at least one slot is needed")
@@ -576,9 +576,9 @@ def _cache(k_cache, v_cache, dtype, dev):
         raise ValueError("k_cache and v_cache must be [pages, page, Hkv, D] tensors of the same strides")
     if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise ValueError(f"k_cache and v_cache must be {dtype}")
-    if k_cache.device != dev or v_cache.device != dev:
-        _on_device(k_cache, dev, "k_cache")
-        _on_device(v_cache, dev, "v_cache")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        _on_device(k_cache, _torch.device("cuda", dev), "k_cache")
+        _on_device(v_cache, _torch.device("cuda", dev), "v_cache")
     return k_cache.shape
 
 
@@ -590,10 +590,11 @@ def cache_store(k, v, slots, k_cache, v_cache):
     skips its token), k_cache, v_cache [pages, page, Hkv, D]. Returns (k_cache, v_cache).
     """
     _get_torch()
-    dev = k.device
     if not k.is_cuda:
         raise ValueError("k must be a device tensor")
-    _on_device(v, dev, "v")
+    dev = k.get_device()
+    if v.get_device() != dev:
+        _on_device(v, k.device, "v")
     if k.dim() < 3 or k.shape != v.shape or k.dtype is not v.dtype:
         raise ValueError("k and v must be [..., Hkv, D] tensors of one shape and type")
     if slots.shape != k.shape[:-2]:
@@ -615,19 +616,19 @@ def _attention_args(q, Hkv, scale, out, lse, workspace, dev):
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = _torch.empty(shape, dtype=q.dtype, device=dev)
-    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
-        _on_device(out, dev, "out")
+        out = _torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        _on_device(out, q.device, "out")
         raise ValueError("out must be a contiguous tensor of q's shape and type")
     lp = None
     if lse is not None:
-        if lse.shape != shape[:3] or lse.dtype is not _torch.float32 or not lse.is_contiguous() or lse.device != dev:
-            _on_device(lse, dev, "lse")
+        if lse.shape != shape[:3] or lse.dtype is not _torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+            _on_device(lse, q.device, "lse")
             raise ValueError("lse must be a contiguous float32 [B, N, Hq] tensor")
         lp = lse.data_ptr()
     wp, wn = None, 0
     if workspace is not None:
-        _check_workspace(workspace, dev, 0)
+        _check_workspace(workspace, q.device, 0)
         wp, wn = workspace.data_ptr(), workspace.numel()
     return scale, out, lp, wp, wn
 
@@ -645,9 +646,9 @@ def tree_attention(q, k_cache, v_cache, table, cache_lens, parents=None, sizes=N
     capture. Returns (out, lse); lse None unless supplied.
     """
     _get_torch()
-    dev = q.device
     if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")
+    dev = q.get_device()
     B, N, Hq, D = q.shape
     pages, page, Hkv, Dk = _cache(k_cache, v_cache, q.dtype, dev)
     if Dk != D:
@@ -670,21 +671,21 @@ def cross_attention(q, k, v, lens=None, key_mask=None, scale=None, out=None, lse
     tree_attention. Returns (out, lse).
     """
     torch = _get_torch()
-    dev = q.device
     if not q.is_cuda or q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and k, v [B, S, Hkv, D]")
+    dev = q.get_device()
     if k.dtype is not q.dtype or v.dtype is not q.dtype:
         raise ValueError("q, k and v must have one type")
-    if k.device != dev or v.device != dev:
-        _on_device(k, dev, "k")
-        _on_device(v, dev, "v")
+    if k.get_device() != dev or v.get_device() != dev:
+        _on_device(k, q.device, "k")
+        _on_device(v, q.device, "v")
     B, N, Hq, D = q.shape
     _, S, Hkv, _ = k.shape
     if k.shape[0] != B or k.shape[3] != D:
         raise ValueError("k and v must have q's batch and head size")
     mp = None
     if key_mask is not None:
-        _on_device(key_mask, dev, "key_mask")
+        _on_device(key_mask, q.device, "key_mask")
         if key_mask.shape != (B, S) or key_mask.dtype not in (torch.uint8, torch.bool) or not key_mask.is_contiguous():
             raise ValueError("key_mask must be a contiguous [B, S] uint8/bool tensor")
         mp = key_mask.data_ptr()
