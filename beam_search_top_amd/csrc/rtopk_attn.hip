@@ -31,6 +31,7 @@ template <int DT> struct Elem;
 template <> struct Elem<1> {
     typedef _Float16 T;
     static constexpr uint32_t kExp = 0x7c00u; // exponent bits: all set in infinities and NaN
+    static constexpr float kBelow = 11.f, kTop = 15.9f; // see raised()
     typedef T V8 __attribute__((ext_vector_type(8)));
     typedef T V2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c)
@@ -41,6 +42,7 @@ template <> struct Elem<1> {
 template <> struct Elem<2> {
     typedef __bf16 T;
     static constexpr uint32_t kExp = 0x7f80u;
+    static constexpr float kBelow = 0.f, kTop = 8.f;
     typedef T V8 __attribute__((ext_vector_type(8)));
     typedef T V2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c)
@@ -119,13 +121,36 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // 32 requests x 64 nodes x 4 heads over 1500-4000 keys: 156 us, of which the
 // longest requests take 1.45 times the mean (one workgroup per CU).
 //
-// The running maximum m of a row moves only when a tile exceeds it by more
-// than 2^8 (weights then stay below 2^8, which costs no precision), which makes
-// the rescaling of the accumulators rare. Weights are rounded to the inputs'
-// type, because the matrix instructions take nothing else next to it: half a
-// step per weight, as much as the output's own rounding. Their sum is of the
-// unrounded ones, in float32.
-constexpr float kLazy = 8.f;
+// Weights are 2^(x - m), with the reference m of raised(). They are rounded to the
+// inputs' type, because the matrix instructions take nothing else next to it:
+// half a step per weight, as much as the output's own rounding (float16: down to
+// 2^-25 of the row's largest). Their sum is of the unrounded ones, in float32.
+
+// A row's reference after a tile whose largest score (base 2) is mx: as before,
+// or kBelow under mx. It moves only when a tile exceeds it by more than kTop, so
+// that the accumulators are rarely rescaled; weights stay below 2^kTop. bfloat16
+// has float32's exponents, and all its bits for any weight. float16 has all of its
+// from 2^-14 to 2^15.99 only, so m lies 11 below the largest score and weights
+// use that whole range: those down to 2^-25 of the row's largest keep their
+// bits, and those below 2^-36 become zero. (With m at the largest score the bounds
+// are 2^-14 and 2^-25: 6000 keys 17 nats under one whose own value is zero gave an
+// output 44 % off.) The room of 2^4.9 above is what random scores need not to move m
+// again: with 13 below, 8 x 2048 rows over 1000-2000 keys take 261.5 us, with 11 259.2,
+// at the largest score 260.2. Sums and outputs carry the same factor, which o / l and
+// m + log2(l) take back.
+template <typename E> __device__ __forceinline__ float raised(float m, float mx)
+{
+    float to = mx - E::kBelow;
+    to = mx - to > E::kTop ? mx : to; // where mx has no bits left for kBelow
+    return to > m ? to : m;
+}
+
+// A row's lse from its reference and sum. kBelow is taken off both first, where
+// that is exact: log2(l) near 11 would round a small lse to a multiple of 2^-20.
+template <typename E> __device__ __forceinline__ float row_lse(float m, float l)
+{
+    return l == 0.f ? -INFINITY : (m + E::kBelow + __builtin_log2f(E::kBelow == 0.f ? l : l * (1.f / (1 << (int)E::kBelow)))) * kLn2;
+}
 
 // Tiles in each ring: as many as the LDS of a CU holds for one workgroup of
 // eight waves, or two for each of two workgroups of four.
@@ -504,7 +529,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
                 for (int i = 0; i < 16; ++i)
                     x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : -INFINITY;
         }
-        // ---- the running maximum; scores of the next tile (the last tile's are of whatever
+        // ---- the running reference; scores of the next tile (the last tile's are of whatever
         // lies there, and not used)
         if constexpr (KB > 1)
             y[0] = scores(ks, 0);
@@ -519,8 +544,8 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
             mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
         }
         mx *= cs;
-        if (__any(mx > m + kLazy)) {
-            const float mn = mx > m ? mx : m;
+        if (__any(mx - m > E::kTop)) {
+            const float mn = raised<E>(m, mx);
             const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn); // from -inf: 0
             m = mn;
             l *= f;
@@ -657,7 +682,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
                 }
             }
         if (a.lse && half == 0)
-            a.lse[at] = l == 0.f ? -INFINITY : (m + __builtin_log2f(l)) * kLn2;
+            a.lse[at] = row_lse<E>(m, l);
     } else {
         const int64_t at = ((((int64_t)b * a.Hkv + hk) * a.nsplit + split) * a.N * a.G + row);
         float *po = a.part + at * DP;
@@ -1070,8 +1095,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
                 for (int i = 0; i < 4; ++i)
                     mx = fmaxf(mx, x[n][k][i]);
             mx = rows_max(mx) * cs;
-            if (__any(mx > m[n] + kLazy)) {
-                const float mn = mx > m[n] ? mx : m[n];
+            if (__any(mx - m[n] > E::kTop)) {
+                const float mn = raised<E>(m[n], mx);
                 const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
                 m[n] = mn;
                 l[n] *= f;
@@ -1178,7 +1203,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             *reinterpret_cast<uint64_t *>(static_cast<T *>(a.out) + at * a.D + e) = __builtin_bit_cast(uint64_t, z);
         }
         if (a.lse && e == 0)
-            a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_log2f(L)) * kLn2;
+            a.lse[at] = row_lse<E>(M, L);
     };
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -1326,7 +1351,7 @@ template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn
         *reinterpret_cast<uint64_t *>(static_cast<T *>(a.out) + at * a.D + 4 * lane) = __builtin_bit_cast(uint64_t, y);
     }
     if (a.lse && lane == 0)
-        a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_log2f(L)) * kLn2;
+        a.lse[at] = row_lse<Elem<DT>>(M, L);
 }
 
 template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, const AttnPlan &p, hipStream_t s)

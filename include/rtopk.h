@@ -446,9 +446,12 @@ int rtopk_cache_store(const void *k, const int64_t *k_strides, const void *v, co
  * touch it, whatever its key and value hold (infinities and NaN included). A
  * row that sees no key (or none with x > -inf) gives out = 0 and lse = -inf.
  * Scores, sums and outputs are accumulated in float32, weights rounded to the
- * type of q for the product with the values. The same call gives the same
- * bits. N <= 256, D a multiple of 8 up to 256, Hkv divides Hq, pointers
- * 16-byte aligned (int32 and float arrays 4-byte), strides multiples of 8.
+ * type of q for the product with the values. float16 weights keep their bits
+ * down to 2^-25 of the row's largest and are zero there below 2^-36. An
+ * infinite value that a row does see makes that output infinite, or NaN where
+ * its weight rounds to zero. The same call gives the same bits. N <= 256, D a
+ * multiple of 8 up to 256, Hkv divides Hq, pointers 16-byte aligned (int32 and
+ * float arrays 4-byte), strides multiples of 8.
  * Workspace: as rtopk_cross_attention.
  */
 int rtopk_tree_attention(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
