@@ -145,6 +145,12 @@ template <typename E> __device__ __forceinline__ float raised(float m, float mx)
     return to > m ? to : m;
 }
 
+// Whether a reference is so large that the exponent's argument has to be taken from
+// the rounded score x cs, as m was, and not from x cs in full (one instruction
+// less): the two differ by half a step of m, which from 2^28 on is a factor of 2^16
+// and more, so that the largest weight overflows or vanishes.
+__device__ __forceinline__ bool far_off(float m) { return fabsf(m) >= 1048576.f && m != -INFINITY; }
+
 // A row's lse from its reference and sum. kBelow is taken off both first, where
 // that is exact: log2(l) near 11 would round a small lse to a multiple of 2^-20.
 template <typename E> __device__ __forceinline__ float row_lse(float m, float l)
@@ -199,7 +205,7 @@ __device__ __forceinline__ void values_operand(V8 (&v)[DB], const int (&at)[DB],
 }
 
 template <int DT, int DP, int WR, bool TREE>
-__global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tiles(const AttnArgs a)
+__global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) void attn_tiles(const AttnArgs a)
 {
     typedef Elem<DT> E;
     typedef typename E::T T;
@@ -280,7 +286,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
             q[c] = __builtin_bit_cast(V8, x);
         }
     }
-    const float cs = fabsf(a.scale) * kLog2e;
+    const float cs = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(fabsf(a.scale) * kLog2e)));
 
     // ---- ancestors, by pointer doubling: after round r, s_up[i] holds the
     // nearest 2^r nodes above i (i among them) and s_jump[i] the next one
@@ -457,6 +463,8 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
     for (int d = 0; d < DB; ++d)
         o[d] = f32x16{};
     float m = -INFINITY, l = 0.f;
+    bool far = false; // a row of the wave has a reference far off: then scores are multiplied by cs on their own
+    float by = 1.f, ce = cs; // (by), and in the exponent's argument by 1 (ce)
 
     // this lane's operand addresses: K row `col`, and the V rows of its 16-lane group
     const int kaddr = col * ROWB;
@@ -519,7 +527,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
         const uint64_t all = BN == 64 ? ~0ull : (1ull << BN) - 1;
         uint64_t see = oks[0];
         const bool masked = see != all || in_tree;
-        if (masked) {
+        if (masked || far) {
             if (in_tree)
                 see &= window(t * BN);
             const uint64_t bits = see >> (4 * half);
@@ -527,7 +535,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
             for (int k = 0; k < KB; ++k)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] : -INFINITY;
+                    x[k][i] = bits >> (32 * k + 8 * (i / 4) + i % 4) & 1 ? x[k][i] * by : -INFINITY;
         }
         // ---- the running reference; scores of the next tile (the last tile's are of whatever
         // lies there, and not used)
@@ -543,11 +551,19 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
             const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
             mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
         }
-        mx *= cs;
+        mx *= ce;
         if (__any(mx - m > E::kTop)) {
             const float mn = raised<E>(m, mx);
             const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn); // from -inf: 0
             m = mn;
+            if (!far && __any(far_off(m))) {
+                far = true;
+                by = cs;
+                ce = 1.f;
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+                    x[k] *= cs;
+            }
             l *= f;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -561,7 +577,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || WR < 4 ? 1 : 2) void attn_tile
         for (int k = 0; k < KB; ++k)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                x[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][i], cs, -mu));
+                x[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][i], ce, -mu));
         if (masked && cs == 0.f) { // 0 * -inf is not -inf
             const uint64_t bits = see >> (4 * half);
 #pragma unroll
@@ -1001,7 +1017,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             for (int c = 0; c < DC; ++c)
                 q[n][c] ^= 0x80008000u;
     }
-    const float cs = fabsf(a.scale) * kLog2e;
+    const float cs = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(fabsf(a.scale) * kLog2e)));
     // the nodes that each of its rows sees (at most 32 nodes: R <= 16 NB)
     const bool walk = TREE && kr.size > 1 && t_end * kFewStep > kr.tree0;
     uint32_t up[NB] = {};
@@ -1024,9 +1040,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
     const int kr0 = 4 * (col & 3) + (col >> 2);
 
     f32x4 o[NB][VE];
-    float m[NB], l[NB];
+    float m[NB], l[NB], ce[NB];
+    bool far[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
+        far[n] = false;
+        ce[n] = cs;
         m[n] = -INFINITY;
         l[n] = 0.f;
 #pragma unroll
@@ -1081,7 +1100,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
                 see[n] &= off < 0 ? (up[n] << -off) | ((1u << -off) - 1) : off < 32 ? up[n] >> off : 0;
             }
             const uint32_t bits = see[n] >> grp;
-            if (masked) {
+            if (masked || far[n]) {
+                if (far[n]) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        x[n][k] *= cs;
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -1094,11 +1118,18 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     mx = fmaxf(mx, x[n][k][i]);
-            mx = rows_max(mx) * cs;
+            mx = rows_max(mx) * ce[n];
             if (__any(mx - m[n] > E::kTop)) {
                 const float mn = raised<E>(m[n], mx);
                 const float f = m[n] == mn ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
                 m[n] = mn;
+                if (!far[n] && __any(far_off(mn))) {
+                    far[n] = true;
+                    ce[n] = 1.f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        x[n][k] *= cs;
+                }
                 l[n] *= f;
 #pragma unroll
                 for (int y = 0; y < VE; ++y)
@@ -1110,7 +1141,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k][i], cs, -mu));
+                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k][i], ce[n], -mu));
                     if (masked && cs == 0.f) // 0 * -inf is not -inf
                         e = bits >> (16 * k + 4 * i) & 1 ? e : 0.f;
                     l[n] += e;

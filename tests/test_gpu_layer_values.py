@@ -1,4 +1,5 @@
-"""Attention outputs where a lost weight shows. References in 64 bits."""
+"""Attention outputs where a lost weight or an extreme score shows. References in
+64 bits."""
 import math
 
 import pytest
@@ -131,3 +132,35 @@ def test_seen_infinities_spoil_their_column_only():
         assert not torch.isfinite(out[..., 3]).any()
         want = v[0, 7, 0].cpu().double()[keep]
         assert ((out[0, :, 0][:, keep] - want).abs() <= 2.02 * HALF[F16] * want.abs() + 1e-12).all()
+
+
+# ------------------------------------------------------------------ scores near the largest floats
+@pytest.mark.parametrize("dt,top", [(F16, 2.0 ** 15), (BF16, 2.0 ** 15), (BF16, 2.0 ** 20), (BF16, 2.0 ** 55)])
+@pytest.mark.parametrize("N", [1, 20, 40, 70, 300])
+def test_far_scores(dt, top, N):
+    """Scores from 2^30 to beyond 2^110, where a float32 has no bits left for
+    differences of a few nats: one key wins by a large factor (two share it where
+    they are equal), and the output is its value, rounded as a weight and once."""
+    D, S = 64, 300
+    print(f"[far scores] {dt} top={top} N={N}", flush=True)
+    g = _gen(N)
+    v = _rnd(g, 1, S, 1, D, dt=dt)
+    vd = v[0, :, 0].cpu().double()
+    for sign in (1.0, -1.0):
+        for scale in (0.125, 0.1, -0.3):
+            for first in (5, 250):
+                # the winner's size times 1.5 where the score is positive, times 1/4 where negative
+                wins = sign * scale > 0
+                size = torch.full((S,), 0.75, device=DEV) - 0.25 * torch.rand(S, generator=g, device=DEV)
+                size[first] = 1.5 if wins else 0.25
+                size[first + 1] = size[first] if first == 250 else size[first + 1]
+                k = (sign * size * top)[None, :, None, None].expand(1, S, 1, D).to(dt).contiguous()
+                q = torch.full((1, N, 1, D), top, device=DEV).to(dt)
+                out, lse = _cross(q, k, v, scale=scale)
+                x = k[0, :, 0, 0].cpu().double() * q[0, 0, 0, 0].item() * D * scale
+                want = vd[[first, first + 1]].mean(0) if first == 250 else vd[first]
+                mag = vd[[first, first + 1]].abs().mean(0) if first == 250 else vd[first].abs()
+                what = f"sign {sign} scale {scale} first {first}"
+                assert int(x.argmax()) in (first, first + 1), what
+                assert ((out[0, :, 0] - want).abs() <= 2.02 * HALF[dt] * mag).all(), what
+                assert ((lse[0, :, 0] - x.max()).abs() <= F * (D + 8) * x.max().abs()).all(), what
