@@ -451,7 +451,7 @@ int rtopk_cache_store(const void *k, const int64_t *k_strides, const void *v, co
  * infinite value that a row does see makes that output infinite, or NaN where
  * its weight rounds to zero. The same call gives the same bits. N <= 256, D a
  * multiple of 8 up to 256, Hkv divides Hq, pointers 16-byte aligned (int32 and
- * float arrays 4-byte), strides multiples of 8.
+ * float arrays 4-byte), strides multiples of 8, scale between -2^127 and 2^127.
  * Workspace: as rtopk_cross_attention.
  */
 int rtopk_tree_attention(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
