@@ -74,7 +74,7 @@ int check_attention(const char *what, int dtype, int B, int N, int Hq, int Hkv, 
         return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (B=%d N=%d Hq=%d Hkv=%d D=%d)", what, B, N, Hq, Hkv, D);
     if (Hq % Hkv)
         return set_error(RTOPK_EINVAL, "%s: Hq=%d is not a multiple of Hkv=%d", what, Hq, Hkv);
-    if (!(std::fabs(scale) <= 0x1p127f)) // so that scale * log2(e) is finite too
+    if (!std::isfinite(scale) || std::fabs(scale) > 0x1p127f) // so that scale * log2(e) is finite too
         return set_error(RTOPK_EINVAL, "%s: scale must be finite, at most 2^127", what);
     if (dtype == RTOPK_F32)
         return set_error(RTOPK_ENOTSUP, "%s: float32 is not supported, only float16 and bfloat16", what);
