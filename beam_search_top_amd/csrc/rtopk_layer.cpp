@@ -104,8 +104,9 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
     if (workspace && ws_bytes < p.ws_bytes)
         return set_error(RTOPK_ENOMEM, "%s: workspace of %zu bytes is smaller than the %zu needed", what, ws_bytes,
                          p.ws_bytes);
-    if (p.grid > INT_MAX)
-        return set_error(RTOPK_ENOTSUP, "%s: %lld workgroups exceed one launch", what, (long long)p.grid);
+    if (p.grid > (int64_t)UINT32_MAX / (64 * p.waves)) // a launch counts its threads in 32 bits
+        return set_error(RTOPK_ENOTSUP, "%s: %lld workgroups of %d threads exceed one launch", what, (long long)p.grid,
+                         64 * p.waves);
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
     a.min_tiles = p.min_tiles;

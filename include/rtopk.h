@@ -470,6 +470,8 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
  *   lens       device [B] int32, held to [0, S]; NULL = S
  *   key_mask   device [B][S] uint8, nonzero = left out; NULL = none
  *   out, lse   as rtopk_tree_attention (N any, B*N*Hq*D < 2^31)
+ * Both attentions answer RTOPK_ENOTSUP where a launch would have 2^32 threads
+ * (with up to 32 rows per key head from 2^24 of B*Hkv on).
  * Workspace: keys are split over workgroups when there are few rows, and the
  * parts are joined in a fixed order. workspace NULL uses the library-owned
  * workspace of `stream` (as rtopk_beam_step; calls that use one stream's come

@@ -13,3 +13,11 @@ def test_scales_whose_base_2_form_overflows_are_refused(lib, scale):  # noqa: F8
     for fn, base in ((rtopk.rtopk_tree_attention, TREE), (rtopk.rtopk_cross_attention, CROSS)):
         st, err = _call(fn, list(base), base, dict(scale=scale))
         assert st == E and "scale" in err, err
+
+
+@pytest.mark.parametrize("B,Hkv", [(1 << 24, 1), (1 << 23, 2), (1 << 22, 8)])
+def test_more_threads_than_one_launch_takes_are_refused(lib, B, Hkv):  # noqa: F811
+    # a workgroup of 256 threads per batch element and key head: 2^32 of them, which a launch cannot count
+    for fn, base in ((rtopk.rtopk_tree_attention, TREE), (rtopk.rtopk_cross_attention, CROSS)):
+        st, err = _call(fn, list(base), base, dict(B=B, N=1, Hq=Hkv, Hkv=Hkv, D=8))
+        assert st == N and "one launch" in err, err
