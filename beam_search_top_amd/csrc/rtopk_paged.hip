@@ -272,9 +272,8 @@ hipError_t launch_page_tables(const TableArgs &a, hipStream_t s)
 
 hipError_t launch_cache_store(StoreArgs a, int unit_bytes, hipStream_t s)
 {
-    // tokens per workgroup: one round of its lanes, and at least one token
-    const int per = kStoreThreads * kStoreVecs;
-    a.tpw = (int)a.row.d >= per ? 1 : per / (int)a.row.d;
+    static_assert(kStoreThreads == 256, "store_tokens");
+    a.tpw = (int)store_tokens(a.T, a.row.d, kStoreThreads * kStoreVecs);
     const int64_t blocks = (a.T + a.tpw - 1) / a.tpw;
     if (unit_bytes == 16)
         hipLaunchKernelGGL(cache_store<u32x4>, dim3((unsigned)blocks), dim3(kStoreThreads), 0, s, a);

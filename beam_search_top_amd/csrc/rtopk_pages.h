@@ -74,6 +74,15 @@ RTOPK_HD int32_t slot_of(int32_t id, int num_pages, int page, int off)
     return checked_page(id, num_pages) < 0 ? -1 : id * page + off; // num_pages * page < 2^31
 }
 
+// Tokens per workgroup of the store: as many rows of `row` units as one round of its
+// lanes moves (`round` units), at least one, and more where T tokens would take 2^24
+// workgroups of 256 threads: a launch counts its threads in 32 bits.
+inline int64_t store_tokens(int64_t T, int64_t row, int64_t round)
+{
+    const int64_t most = (1 << 24) - 1, least = (T + most - 1) / most, per = row >= round ? 1 : round / row;
+    return per > least ? per : least;
+}
+
 // Node i's parent: a value outside [0, i) is no parent.
 RTOPK_HD int parent_of(int32_t p, int i) { return p >= 0 && p < i ? p : -1; }
 

@@ -164,3 +164,24 @@ def test_far_scores(dt, top, N):
                 assert int(x.argmax()) in (first, first + 1), what
                 assert ((out[0, :, 0] - want).abs() <= 2.02 * HALF[dt] * mag).all(), what
                 assert ((lse[0, :, 0] - x.max()).abs() <= F * (D + 8) * x.max().abs()).all(), what
+
+
+# ------------------------------------------------------------------ more tokens than a launch has workgroups
+def test_store_of_2_to_the_24_tokens():
+    # overlapping rows of 4 x 257 elements, so that every token differs; few of them have a slot
+    T, H, D, page, pages = (1 << 24) + 5, 4, 257, 16, 6
+    g = _gen(3)
+    buf = _rnd(g, T + H * D + 7)
+    k = torch.as_strided(buf, (T, H, D), (1, D, 1))
+    v = torch.as_strided(buf, (T, H, D), (1, D, 1), 7)
+    slots = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    at = torch.cat([torch.tensor([0, 1, T - 1, T - 2, T // 2, (1 << 24) - 1, 1 << 24], device=DEV),
+                    torch.randint(2, T // 2, (60,), generator=g, device=DEV).unique()])
+    slots[at] = torch.randperm(pages * page, generator=g, device=DEV)[:at.numel()].to(torch.int32)
+    kc, vc = torch.full((pages, page, H, D), 3.0, dtype=F16, device=DEV), torch.full((pages, page, H, D), 4.0, dtype=F16, device=DEV)
+    wk, wv = kc.clone().view(-1, H, D), vc.clone().view(-1, H, D)
+    wk[slots[at].long()], wv[slots[at].long()] = k[at], v[at]
+    print("[store] 2^24 tokens", flush=True)
+    rtopk.cache_store(k, v, slots, kc, vc)
+    torch.cuda.synchronize()
+    assert torch.equal(kc.view(-1, H, D), wk) and torch.equal(vc.view(-1, H, D), wv)
