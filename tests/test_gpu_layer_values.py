@@ -1,12 +1,15 @@
-"""Attention outputs where a lost weight or an extreme score shows. References in
-64 bits."""
+"""Attention outputs where a wrong value, a lost weight or an extreme score shows:
+weights far below the largest, every key counted once, rows that pick one key
+out of many, NaN keys, scores near the largest floats; a store of more tokens
+than a launch has workgroups. References in 64 bits."""
 import math
 
 import pytest
 import torch
 
 from beam_search_top_amd import rtopk
-from test_gpu_layer import DEV, _gen, _rnd, lib  # noqa: F401
+from layer_ref import check_tree
+from test_gpu_layer import DEV, _gen, _rnd, _tree, _tree_inputs, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -132,6 +135,142 @@ def test_seen_infinities_spoil_their_column_only():
         assert not torch.isfinite(out[..., 3]).any()
         want = v[0, 7, 0].cpu().double()[keep]
         assert ((out[0, :, 0][:, keep] - want).abs() <= 2.02 * HALF[F16] * want.abs() + 1e-12).all()
+
+
+# ------------------------------------------------------------------ every key counted once
+def _whole(shape, seed, dt):
+    return torch.randint(-8, 9, shape, generator=_gen(seed), device=DEV).to(dt)
+
+
+def _check_means(out, lse, total, count, dt, what):
+    """All scores are zero, so that weights are equal, and values are whole: the sums
+    are exact, and an output is rounded by the reciprocal, the product, an
+    exponential (together 4 f) and once to its type."""
+    want = torch.where(count > 0, total / count.clamp(min=1), 0.0)
+    assert ((out - want).abs() <= (HALF[dt] * 1.01 + 4 * F) * want.abs()).all(), what
+    full = (count[..., 0] > 0).expand(lse.shape)
+    wl = torch.log(count[..., 0].clamp(min=1)).expand(lse.shape)
+    assert torch.equal(lse == -math.inf, ~full) and ((lse - wl).abs() <= 4 * F * wl + F)[full].all(), what
+
+
+@pytest.mark.parametrize("N,D,dt", [(1, 64, F16), (1, 128, BF16), (20, 128, F16), (20, 64, BF16), (40, 64, F16), (70, 128, BF16),
+                                    (300, 128, F16), (300, 64, BF16), (40, 256, BF16), (7, 80, F16)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_cross_every_key_counts_once(N, D, dt, masked):
+    B, S, H = 3, 40007, 1
+    lens = [40007, 12345, 33]
+    print(f"[cross counts] N={N} D={D} {dt} masked={masked}", flush=True)
+    g = _gen(N)
+    q, k, v = _rnd(g, B, N, H, D, dt=dt), _rnd(g, B, S, H, D, dt=dt), _whole((B, S, H, D), N + D, dt)
+    mask = (torch.rand(B, S, generator=g, device=DEV) < 0.3) if masked else None
+    out, lse = _cross(q, k, v, lens=torch.tensor(lens, dtype=torch.int32, device=DEV), key_mask=mask, scale=0.0)
+    ok = torch.arange(S)[None] < torch.tensor(lens)[:, None]
+    if masked:
+        ok &= ~mask.cpu()
+    vd = torch.where(ok[:, :, None, None], v.cpu().double(), 0.0)
+    _check_means(out, lse, vd.sum(1)[:, None], ok.sum(1).double()[:, None, None, None], dt, "cross")
+
+
+@pytest.mark.parametrize("N,Hq,D,page,dt", [(1, 2, 64, 16, F16), (1, 16, 128, 64, BF16), (6, 4, 128, 16, F16), (1, 2, 64, 24, BF16),
+                                            (1, 4, 128, 7, F16), (40, 2, 64, 16, F16), (70, 2, 128, 24, BF16), (33, 8, 128, 16, F16),
+                                            (64, 8, 64, 5, BF16), (40, 2, 256, 16, F16)])
+def test_tree_every_key_counts_once(N, Hq, D, page, dt):
+    B, Hkv = 3, 2
+    lens = [20011, 0, 7000]
+    print(f"[tree counts] N={N} Hq={Hq} D={D} page={page} {dt}", flush=True)
+    c = _tree_inputs(B, N, Hq, Hkv, D, page, lens, dt, seed=N + D, tree=N > 1)
+    c["vc"].copy_(_whole(c["vc"].shape, 5, dt))
+    lse = torch.full((B, N, Hq), 7.0, device=DEV)
+    out, _ = rtopk.tree_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], parents=c["parents"], scale=0.0, lse=lse)
+    torch.cuda.synchronize()
+    out, lse, vd, tab = out.cpu().double(), lse.cpu().double(), c["vc"].cpu().double(), c["table"].cpu().long()
+    for b, L in enumerate(lens):
+        at = torch.arange(L + N)
+        v = vd[tab[b, at // page], at % page]  # [L + N, Hkv, D]
+        total, count = torch.zeros(N, Hkv, D, dtype=torch.float64), torch.zeros(N, dtype=torch.float64)
+        for i in range(N):
+            p = -1 if c["parents"] is None else int(c["parents"][b, i])
+            total[i] = (total[p] if p >= 0 else v[:L].sum(0)) + v[L + i]
+            count[i] = (count[p] if p >= 0 else L) + 1
+        _check_means(out[b], lse[b], total.repeat_interleave(Hq // Hkv, 1), count[:, None, None], dt, f"tree b={b}")
+
+
+# ------------------------------------------------------------------ rows that pick one key out of many
+def _pick(S, n, seed):
+    """n positions: the ends of the keys, ends of pieces of 8, 24, 32 and 64, any others."""
+    g = torch.Generator().manual_seed(seed)
+    edge = torch.randint(0, S // 64, (n,), generator=g) * 64
+    off = torch.tensor([0, -1, 8, 23, 24, 31, 32, 63])[torch.randint(0, 8, (n,), generator=g)]
+    p = torch.where(torch.rand(n, generator=g) < 0.7, edge + off, torch.randint(0, S, (n,), generator=g)).clamp(0, S - 1)
+    p[0], p[-1] = S - 1, 0
+    return p
+
+
+def _signs(shape, seed, dt):
+    return (torch.randint(0, 2, shape, generator=_gen(seed), device=DEV) * 2 - 1).to(dt)
+
+
+def _check_picks(out, lse, v, at, D, dt, what):
+    """A row is 8 times the signs of its key: that key's score is 8 sqrt(D), another's
+    8 times a normal variable. The weights of the others sum up to less than 2^-13
+    (asserted on the scores by the caller), which moves an output by less than 2^-13 of
+    two values (at most 6 each); the rest is rounding: twice half a step."""
+    want = v[at]
+    assert ((out - want).abs() <= 2.02 * HALF[dt] * want.abs() + 2.0 ** -13 * 12).all(), what
+    assert ((lse - 8 * D ** 0.5).abs() <= 2.0 ** -13 + F * 8 * D ** 0.5 * (D + 8)).all(), what
+
+
+@pytest.mark.parametrize("N,D,dt", [(1, 64, F16), (32, 64, F16), (32, 128, BF16), (16, 128, F16), (64, 128, BF16), (100, 64, F16),
+                                    (500, 64, BF16), (500, 128, F16), (60, 256, BF16)])
+def test_cross_rows_pick_a_key(N, D, dt):
+    S = 50021
+    k, v = _signs((1, S, 1, D), D, dt), _rnd(_gen(D), 1, S, 1, D, dt=dt)
+    kd, vd = k[0, :, 0].cpu().float(), v[0, :, 0].cpu().double()
+    for rep in range(6 if N < 100 else 2):
+        print(f"[cross picks] N={N} D={D} {dt} rep={rep}", flush=True)
+        at = _pick(S, N, 100 * rep + D)
+        q = (8 * k[0, at.to(DEV)])[None].contiguous()
+        x = (8 * D ** -0.5) * (kd[at] @ kd.T)
+        x[torch.arange(N), at] = -math.inf
+        assert torch.logsumexp(x.double(), 1).max() < 8 * D ** 0.5 - math.log(2 ** 13)
+        out, lse = _cross(q, k, v)
+        _check_picks(out[0, :, 0], lse[0, :, 0], vd, at, D, dt, f"rep {rep}")
+
+
+@pytest.mark.parametrize("N,G,D,page,dt", [(1, 32, 64, 16, F16), (1, 16, 128, 64, BF16), (2, 16, 128, 24, F16), (1, 32, 64, 5, BF16),
+                                           (16, 4, 128, 16, BF16), (29, 4, 64, 24, F16), (64, 4, 128, 16, F16), (20, 2, 256, 16, F16)])
+def test_tree_rows_pick_a_key(N, G, D, page, dt):
+    S = 30011
+    k, v = _signs((1, S, 1, D), D, dt), _rnd(_gen(D), 1, S, 1, D, dt=dt)
+    kd, vd = k[0, :, 0].cpu().float(), v[0, :, 0].cpu().double()
+    for rep in range(4):
+        print(f"[tree picks] N={N} G={G} D={D} page={page} {dt} rep={rep}", flush=True)
+        at = _pick(S - N, N * G, 100 * rep + D)  # before the tree
+        x = (8 * D ** -0.5) * (kd[at] @ kd.T)
+        x[torch.arange(N * G), at] = -math.inf
+        assert torch.logsumexp(x.double(), 1).max() < 8 * D ** 0.5 - math.log(2 ** 13)
+        q = (8 * k[0, at.to(DEV), 0]).view(1, N, G, D)
+        out, lse = _tree1(q, k, v, page, rep)
+        _check_picks(out[0].reshape(N * G, D), lse[0].reshape(-1), vd, at, D, dt, f"rep {rep}")
+
+
+# ------------------------------------------------------------------ keys with NaN that some rows see
+@pytest.mark.parametrize("N,dt,G", [(8, F16, 1), (8, BF16, 4), (70, F16, 2), (200, BF16, 1)])
+def test_tree_nan_keys_reach_the_rows_that_see_them(N, dt, G):
+    c = _tree_inputs(2, N, 2 * G, 2, 64, 16, [40, 61], dt, seed=N + 1)
+    i = torch.arange(1, N, device=DEV)
+    c["parents"][:, 1:] = torch.where(i % 2 == 0, i - 2, -1).to(torch.int32)  # even nodes below node 0, odd ones alone
+    node3 = [(int(c["table"][b, (L + 3) // 16]), (L + 3) % 16) for b, L in ((0, 40), (1, 61))]
+    clean, clean_lse = _tree(c, "without NaN")
+    kept = c["kc"].clone()
+    for at in node3:
+        c["kc"][at] = math.nan
+    out, lse = torch.full_like(c["q"], 3.0), torch.full((2, N, 2 * G), 5.0, device=DEV)
+    rtopk.tree_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], parents=c["parents"], out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:, 3].float()).all() and torch.isnan(lse[:, 3]).all()
+    out[:, 3], lse[:, 3] = clean[:, 3], clean_lse[:, 3]  # every other row as if the key were any
+    check_tree(c["q"], kept, c["vc"], c["table"], [40, 61], c["parents"], None, 64 ** -0.5, out, lse, "NaN keys")
 
 
 # ------------------------------------------------------------------ scores near the largest floats
