@@ -347,17 +347,21 @@ struct WsEntry {
     void *ptr = nullptr;
     size_t bytes = 0;
 };
+typedef std::map<std::pair<int, void *>, WsEntry> WsMap; // by device and stream
 std::mutex g_ws_mu;
-std::map<std::pair<int, void *>, WsEntry> g_ws;
+WsMap g_ws;
+// The attention calls' own: a captured selection step may hold its stream's
+// workspace, which an attention call that needs more must not free.
+WsMap g_attn_ws;
 
 // With g_ws_mu held.
-int acquire_locked(size_t need, hipStream_t stream, void **out)
+int acquire_locked(WsMap &all, size_t need, hipStream_t stream, void **out)
 {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess)
         return fail(RTOPK_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
-    WsEntry &w = g_ws[{dev, (void *)stream}];
+    WsEntry &w = all[{dev, (void *)stream}];
     if (w.bytes < need) {
         if (w.ptr) {
             // earlier calls on this stream may still use the old buffer
@@ -390,7 +394,7 @@ int acquire_locked(size_t need, hipStream_t stream, void **out)
 int acquire_workspace(size_t need, hipStream_t stream, void **out)
 {
     std::lock_guard<std::mutex> lock(g_ws_mu);
-    return acquire_locked(need, stream, out);
+    return acquire_locked(g_ws, need, stream, out);
 }
 
 // A device buffer of zeros per device (the running scores of sampling rows),
@@ -439,7 +443,7 @@ int rtopk::with_workspace(size_t need, hipStream_t stream, const std::function<i
         return fail(RTOPK_EINVAL, "a captured call needs a workspace of the caller's");
     std::lock_guard<std::mutex> lock(g_ws_mu);
     void *ws = nullptr;
-    const int st = acquire_locked(need, stream, &ws);
+    const int st = acquire_locked(g_attn_ws, need, stream, &ws);
     return st == RTOPK_OK ? launch(ws) : st;
 }
 
@@ -855,16 +859,18 @@ void rtopk_release(void)
 {
     std::lock_guard<std::mutex> lock(g_ws_mu);
     int cur = -1;
-    if (!g_ws.empty() && hipGetDevice(&cur) != hipSuccess)
+    if (!(g_ws.empty() && g_attn_ws.empty()) && hipGetDevice(&cur) != hipSuccess)
         cur = -1;
-    for (auto &kv : g_ws) {
-        if (kv.second.ptr) {
-            (void)hipSetDevice(kv.first.first);
-            (void)hipDeviceSynchronize();
-            (void)hipFree(kv.second.ptr);
+    for (WsMap *all : {&g_ws, &g_attn_ws}) {
+        for (auto &kv : *all) {
+            if (kv.second.ptr) {
+                (void)hipSetDevice(kv.first.first);
+                (void)hipDeviceSynchronize();
+                (void)hipFree(kv.second.ptr);
+            }
         }
+        all->clear();
     }
-    g_ws.clear();
     for (auto &kv : g_zeros) {
         if (kv.second.ptr) {
             (void)hipSetDevice(kv.first);

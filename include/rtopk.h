@@ -473,12 +473,12 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
  * Both attentions answer RTOPK_ENOTSUP where a launch would have 2^32 threads
  * (with up to 32 rows per key head from 2^24 of B*Hkv on).
  * Workspace: keys are split over workgroups when there are few rows, and the
- * parts are joined in a fixed order. workspace NULL uses the library-owned
- * workspace of `stream` (as rtopk_beam_step; calls that use one stream's come
- * from one thread at a time); a call that a graph captures is then refused
- * (RTOPK_EINVAL) if it needs one. A caller's workspace holds
- * ws_bytes >= rtopk_cross_attention_workspace_bytes(...) bytes, 256-byte
- * aligned, zero-filled before its first use (it may be one of
+ * parts are joined in a fixed order. workspace NULL uses a library-owned
+ * workspace of `stream` (as rtopk_beam_step, but one of the attentions' own;
+ * calls that use one stream's come from one thread at a time); a call that a
+ * graph captures is then refused (RTOPK_EINVAL) if it needs one. A caller's
+ * workspace holds ws_bytes >= rtopk_cross_attention_workspace_bytes(...) bytes,
+ * 256-byte aligned, zero-filled before its first use (it may be one of
  * rtopk_beam_step_ws); calls sharing it must be ordered, so graphs that may
  * run at the same time need one each.
  */

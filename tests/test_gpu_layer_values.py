@@ -324,3 +324,39 @@ def test_store_of_2_to_the_24_tokens():
     rtopk.cache_store(k, v, slots, kc, vc)
     torch.cuda.synchronize()
     assert torch.equal(kc.view(-1, H, D), wk) and torch.equal(vc.view(-1, H, D), wv)
+
+
+# ------------------------------------------------------------------ library workspaces
+def test_a_captured_step_keeps_its_library_workspace():
+    """A selection step captured on its stream's library-owned workspace, then
+    attention calls on that stream which need ever more workspace, memory that is
+    allocated and overwritten between replays: every replay as the eager step."""
+    g = _gen(9)
+    B, beam, V, H = 16, 4, 6000, 256
+    hid, w = _rnd(g, B * beam, H, dt=BF16), _rnd(g, V, H, dt=BF16)
+    alive = torch.randn(B, beam, generator=g, device=DEV)
+    want = [o.clone() for o in rtopk.lmhead_step(hid, w, alive, None, k=4)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        rtopk.lmhead_step(hid, w, alive, None, k=4)  # the workspace exists before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = rtopk.lmhead_step(hid, w, alive, None, k=4)
+    q, k = _rnd(g, 2, 32, 8, 128), _rnd(g, 2, 40000, 8, 128)
+    first = rtopk.cross_attention(q, k, k)[0]
+    torch.cuda.synchronize()
+    for rep in range(4):
+        n = 8 * (rep + 1)
+        with torch.cuda.stream(s):
+            out = rtopk.cross_attention(q[:, :n].contiguous(), k, k)[0]
+            junk = torch.full((1 << 24,), math.nan, device=DEV)
+        for o in got:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), rep
+        del junk
+    assert torch.equal(out, first)
