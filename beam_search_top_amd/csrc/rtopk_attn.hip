@@ -115,10 +115,10 @@ __device__ __forceinline__ int tiles_per_split(int tiles, const AttnArgs &a)
 // Bound by the matrix cores and the vector unit together: per 64 keys a wave has
 // 1024 cycles of products and about 1100 of exponentials, maxima, sums and
 // conversions, which overlap only in part. 8 x 2048 rows over 1000-2000 keys, 16
-// heads of 128, bf16: 247 us, 815 TFLOP/s (timing copies: without the softmax
+// heads of 128, bf16: 246 us, 818 TFLOP/s (timing copies: without the softmax
 // 222 us of then 264, without loads 231, products and barriers alone 122). A
 // wave of 64 rows halves the LDS reads but leaves one wave per SIMD: 318 us.
-// 32 requests x 64 nodes x 4 heads over 1500-4000 keys: 156 us, of which the
+// 32 requests x 64 nodes x 4 heads over 1500-4000 keys: 158 us, of which the
 // longest requests take 1.45 times the mean (one workgroup per CU).
 //
 // Weights are 2^(x - m), with the reference m of raised(). They are rounded to the
@@ -811,7 +811,7 @@ template <bool TREE> __device__ __forceinline__ Share find_share(const AttnArgs 
             if (kr.size > 0)
                 tiles[i] = (kr.end + kFewStep - 1) / kFewStep;
         }
-        total += tiles[i] > 0 ? tiles[i] : 0; // at most 256 * 2^26 / 32 per lane group: the host bounds B * S
+        total += tiles[i] > 0 ? tiles[i] : 0; // of all together at most 2^30: the host cuts no call of more
         longest = tiles[i] > longest ? tiles[i] : longest;
     }
 #pragma unroll
