@@ -35,7 +35,12 @@ SAMPLE = os.path.join(CSRC, "rtopk_sample.hip")
 PAGED = os.path.join(CSRC, "rtopk_paged.hip")
 ATTN = os.path.join(CSRC, "rtopk_attn.hip")
 LAYER = os.path.join(CSRC, "rtopk_layer.cpp")
-# the attention kernels have to keep what a NaN means: a masked one is dropped, another spreads
+ROPE = os.path.join(CSRC, "rtopk_rope.hip")
+CACHE8 = os.path.join(CSRC, "rtopk_cache8.hip")
+FILTER = os.path.join(CSRC, "rtopk_filter.hip")
+FILTER_HOST = os.path.join(CSRC, "rtopk_filter.cpp")
+# the attention kernels have to keep what a NaN means: a masked one is dropped, another spreads;
+# so do the rotation, the 8-bit cache and the filters, which store or compare what they read
 ATTN_FLAGS = [f for f in FLAGS if f != "-fno-honor-nans"]
 NOALLOC = os.path.join(CSRC, "rtopk_noalloc.hip")
 DTYPES = (0, 1, 2)  # the kernel source is compiled once per logit type, in parallel
@@ -60,8 +65,12 @@ def _run(cmds, verbose):
 def build(verbose: bool = False, extra=()) -> str:
     tag = f".tmp{os.getpid()}"
     objs = [LIB + f".dt{d}{tag}.o" for d in DTYPES] + [LIB + f".{n}{tag}.o" for n in (
-        "attn", "paged", "layer", "noalloc", "sample", "reorder", "host")]
+        "rope", "cache8", "filter", "filterhost", "attn", "paged", "layer", "noalloc", "sample", "reorder", "host")]
     cmds = [[HIPCC, *FLAGS, *extra, f"-DRTOPK_DTYPE={d}", "-c", KERNELS, "-o", o] for d, o in zip(DTYPES, objs)]
+    cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", ROPE, "-o", objs[-11]])
+    cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", CACHE8, "-o", objs[-10]])
+    cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", FILTER, "-o", objs[-9]])
+    cmds.append([HIPCC, *FLAGS, *extra, "-c", FILTER_HOST, "-o", objs[-8]])
     cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", ATTN, "-o", objs[-7]])
     cmds.append([HIPCC, *FLAGS, *extra, "-c", PAGED, "-o", objs[-6]])
     cmds.append([HIPCC, *FLAGS, *extra, "-c", LAYER, "-o", objs[-5]])

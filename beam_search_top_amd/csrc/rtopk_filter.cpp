@@ -1,0 +1,43 @@
+// Host side of filtered sampling: argument checks and the launch. As elsewhere,
+// a rejected call touches neither the GPU nor its outputs.
+#include "rtopk.h"
+#include "rtopk_filter.h"
+
+using rtopk::set_error;
+
+extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
+                                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                                     int32_t *out_token, float *out_logprob, void *stream)
+{
+    const char *what = "filtered sampling";
+    if (!logits || !u || !out_token || !out_logprob)
+        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
+    if (dtype != RTOPK_F32 && dtype != RTOPK_F16 && dtype != RTOPK_BF16)
+        return set_error(RTOPK_EINVAL, "%s: unknown dtype %d", what, dtype);
+    if (R < 1 || V < 1)
+        return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (R=%d V=%d)", what, R, V);
+    if (ld < 0 || (R > 1 && ld < V) || ld > ((int64_t)1 << 40))
+        return set_error(RTOPK_EINVAL, "%s: rows of %lld elements do not hold V=%d (or are over 2^40)", what, (long long)ld, V);
+    if ((uintptr_t)logits % (dtype == RTOPK_F32 ? 4 : 2))
+        return set_error(RTOPK_EINVAL, "%s: logits are not aligned to their element size", what);
+    if (V > rtopk::kFilterMaxV || R > rtopk::kFilterMaxR)
+        return set_error(RTOPK_ENOTSUP, "%s: V=%d or R=%d exceeds the implementation limits %d and %d", what, V, R,
+                         rtopk::kFilterMaxV, rtopk::kFilterMaxR);
+    rtopk::FilterArgs a{};
+    a.logits = logits;
+    a.R = R;
+    a.V = V;
+    a.ld = ld;
+    a.frac = rtopk::filter_frac(V);
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.out_token = out_token;
+    a.out_logprob = out_logprob;
+    const hipError_t e = rtopk::launch_filter(a, dtype, (hipStream_t)stream);
+    if (e != hipSuccess)
+        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+    return RTOPK_OK;
+}

@@ -3,11 +3,13 @@
 // rejected call touches neither the GPU nor its outputs.
 #include "rtopk.h"
 #include "rtopk_attn.h"
+#include "rtopk_cache8.h"
 
 #include <hip/hip_runtime_api.h>
 
 #include <climits>
 #include <cmath>
+#include <cstring>
 #include <exception>
 
 using rtopk::set_error;
@@ -83,6 +85,49 @@ int check_attention(const char *what, int dtype, int B, int N, int Hq, int Hkv, 
     if (!mul_fits((long long)B * N, Hq, INT_MAX / D))
         return set_error(RTOPK_ENOTSUP, "%s: B*N*Hq*D exceeds 2^31-1", what);
     return RTOPK_OK;
+}
+
+// Whether the rows of D elements of a [n0][n1][D] view with these strides lie apart.
+bool rows_apart(const int64_t st[2], long long n0, long long n1, long long D)
+{
+    const long long s0 = n0 > 1 ? st[0] : LLONG_MAX, s1 = n1 > 1 ? st[1] : LLONG_MAX;
+    const long long small = s0 < s1 ? s0 : s1, large = s0 < s1 ? s1 : s0, n = s0 < s1 ? n0 : n1;
+    return small >= D && (large == LLONG_MAX || large >= (n - 1) * small + D);
+}
+
+// What the 8-bit store and load ask of their sizes and their cache; fills what they share.
+int check_cache8(const char *what, int dtype, int T, int Hkv, int D, const int64_t *cache_strides, int num_pages, int page,
+                 rtopk::Cache8Args &a)
+{
+    if (dtype != RTOPK_F32 && dtype != RTOPK_F16 && dtype != RTOPK_BF16)
+        return set_error(RTOPK_EINVAL, "%s: unknown dtype %d", what, dtype);
+    if (T < 1 || Hkv < 1 || D < 1 || num_pages < 1 || page < 1)
+        return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (T=%d Hkv=%d D=%d num_pages=%d page=%d)", what, T, Hkv, D,
+                         num_pages, page);
+    if (!mul_fits(num_pages, page, INT_MAX))
+        return set_error(RTOPK_EINVAL, "%s: num_pages*page exceeds 2^31-1", what);
+    if (D > rtopk::kMaxRowDim || !mul_fits(Hkv, D, 1 << 20))
+        return set_error(RTOPK_ENOTSUP, "%s: heads of more than %d elements or rows of more than 2^20 (Hkv=%d D=%d)", what,
+                         rtopk::kMaxRowDim, Hkv, D);
+    set_strides(a.cs, cache_strides, page, Hkv, D);
+    if (!strides_fit(a.cs, num_pages, page, Hkv))
+        return set_error(RTOPK_EINVAL, "%s: strides are negative or overflow", what);
+    a.T = T;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.nslots = num_pages * page;
+    a.heads = rtopk::make_page_div((uint32_t)Hkv);
+    a.page = rtopk::make_page_div((uint32_t)page);
+    return RTOPK_OK;
+}
+
+// 16 elements at a time: the codes' rows and the pointers allow 16 bytes.
+bool cache8_wide(const rtopk::Cache8Args &a)
+{
+    bool wide = a.D % 16 == 0 && (uintptr_t)a.kc % 16 == 0 && (uintptr_t)a.vc % 16 == 0;
+    for (int64_t st : a.cs)
+        wide = wide && st % 16 == 0;
+    return wide;
 }
 
 // Workspace of a call whatever its strides.
@@ -280,6 +325,154 @@ int rtopk_cache_store(const void *k, const int64_t *k_strides, const void *v, co
     a.page = rtopk::make_page_div((uint32_t)page);
     a.nslots = num_pages * page;
     const hipError_t e = rtopk::launch_cache_store(a, wide ? 16 : esz, (hipStream_t)stream);
+    if (e != hipSuccess)
+        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+    return RTOPK_OK;
+}
+
+int rtopk_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, int dtype,
+                       const int32_t *positions, const float *freqs, int rot, int interleaved, const void *q_weight,
+                       const void *k_weight, float eps, int T, int Hq, int Hkv, int D, void *q_out,
+                       const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, void *stream)
+{
+    const char *what = "norm and rotation";
+    if (!q || !k || !positions || !q_out || !k_out || (!freqs && rot > 0))
+        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
+    if (dtype != RTOPK_F32 && dtype != RTOPK_F16 && dtype != RTOPK_BF16)
+        return set_error(RTOPK_EINVAL, "%s: unknown dtype %d", what, dtype);
+    if (T < 1 || Hq < 1 || Hkv < 1 || D < 1)
+        return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (T=%d Hq=%d Hkv=%d D=%d)", what, T, Hq, Hkv, D);
+    if (rot < 0 || rot % 2 || rot > D)
+        return set_error(RTOPK_EINVAL, "%s: rot=%d is not an even number up to D=%d", what, rot, D);
+    uint32_t eps_bits; // by its bits: this file is built without NaN in comparisons
+    memcpy(&eps_bits, &eps, sizeof eps);
+    if (eps_bits >= 0x7f800000u && eps_bits != 0x80000000u)
+        return set_error(RTOPK_EINVAL, "%s: eps must be finite and >= 0", what);
+    if (D > rtopk::kMaxRowDim || T > rtopk::kMaxRopeTokens || Hq > (1 << 20) || Hkv > (1 << 20) ||
+        !mul_fits((long long)Hq + Hkv, D, 1 << 20))
+        return set_error(RTOPK_ENOTSUP, "%s: D=%d over %d, (Hq+Hkv)*D over 2^20 or T=%d over 2^28", what, D, rtopk::kMaxRowDim, T);
+    const int esz = dtype == RTOPK_F32 ? 4 : 2;
+    rtopk::RopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    const auto fill = [&](int64_t to[2], const int64_t *given, int H) {
+        to[0] = given ? given[0] : (int64_t)H * D;
+        to[1] = given ? given[1] : D;
+        const int64_t all[3] = {0, to[0], to[1]};
+        const bool fits = strides_fit(all, 1, T, H);
+        to[0] = T == 1 ? 0 : to[0]; // the stride of one entry says nothing
+        to[1] = H == 1 ? 0 : to[1];
+        return fits;
+    };
+    if (!fill(a.qs, q_strides, Hq) || !fill(a.ks, k_strides, Hkv) || !fill(a.qos, q_out_strides, Hq) ||
+        !fill(a.kos, k_out_strides, Hkv))
+        return set_error(RTOPK_EINVAL, "%s: strides are negative or overflow", what);
+    if (!rows_apart(a.qos, T, Hq, D) || !rows_apart(a.kos, T, Hkv, D))
+        return set_error(RTOPK_EINVAL, "%s: rows of an output overlap", what);
+    if ((q_out == q && (a.qos[0] != a.qs[0] || a.qos[1] != a.qs[1])) || (k_out == k && (a.kos[0] != a.ks[0] || a.kos[1] != a.ks[1])))
+        return set_error(RTOPK_EINVAL, "%s: an output in place of its input needs the input's strides", what);
+    if (q_out == k_out || q_out == k || k_out == q)
+        return set_error(RTOPK_EINVAL, "%s: queries and keys need buffers of their own", what);
+    const int unit = 16 / esz; // elements of 16 bytes
+    bool wide = D % (2 * unit) == 0 && rot % (2 * unit) == 0;
+    for (const void *p : {q, k, (const void *)q_out, (const void *)k_out, q_weight, k_weight}) {
+        if ((uintptr_t)p % esz)
+            return set_error(RTOPK_EINVAL, "%s: a pointer is not aligned to its element size", what);
+        wide = wide && (uintptr_t)p % 16 == 0;
+    }
+    for (const int64_t *st : {a.qs, a.ks, a.qos, a.kos})
+        wide = wide && st[0] % unit == 0 && st[1] % unit == 0;
+    a.positions = positions;
+    a.freqs = freqs;
+    a.qw = q_weight;
+    a.kw = k_weight;
+    a.eps = eps;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.rot = rot;
+    a.interleaved = interleaved != 0;
+    a.heads = rtopk::make_page_div((uint32_t)(Hq + Hkv));
+    const hipError_t e = rtopk::launch_rope(a, dtype, wide, (hipStream_t)stream);
+    if (e != hipSuccess)
+        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+    return RTOPK_OK;
+}
+
+int rtopk_cache_store_fp8(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides, int dtype,
+                          const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache,
+                          const int64_t *cache_strides, uint8_t *k_scales, uint8_t *v_scales, int num_pages, int page,
+                          void *stream)
+{
+    const char *what = "8-bit cache store";
+    if (!k || !v || !slots || !k_cache || !v_cache || !k_scales || !v_scales)
+        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
+    rtopk::Cache8Args a{};
+    const int st = check_cache8(what, dtype, T, Hkv, D, cache_strides, num_pages, page, a);
+    if (st != RTOPK_OK)
+        return st;
+    if (k_cache == v_cache || k_scales == v_scales)
+        return set_error(RTOPK_EINVAL, "%s: keys and values need buffers of their own", what);
+    a.k = k;
+    a.v = v;
+    a.kc = (uint8_t *)k_cache;
+    a.vc = (uint8_t *)v_cache;
+    a.ksc = k_scales;
+    a.vsc = v_scales;
+    a.slots = slots;
+    const auto fill = [&](int64_t to[2], const int64_t *given) {
+        to[0] = given ? given[0] : (int64_t)Hkv * D;
+        to[1] = given ? given[1] : D;
+        const int64_t all[3] = {0, to[0], to[1]};
+        return strides_fit(all, 1, T, Hkv);
+    };
+    if (!fill(a.ks, k_strides) || !fill(a.vs, v_strides))
+        return set_error(RTOPK_EINVAL, "%s: strides are negative or overflow", what);
+    const int esz = dtype == RTOPK_F32 ? 4 : 2;
+    bool wide = cache8_wide(a);
+    for (const void *p : {k, v}) {
+        if ((uintptr_t)p % esz)
+            return set_error(RTOPK_EINVAL, "%s: a pointer is not aligned to its element size", what);
+        wide = wide && (uintptr_t)p % 16 == 0;
+    }
+    for (int64_t x : {a.ks[0], a.ks[1], a.vs[0], a.vs[1]})
+        wide = wide && x * esz % 16 == 0;
+    const hipError_t e = rtopk::launch_cache8_store(a, dtype, wide, (hipStream_t)stream);
+    if (e != hipSuccess)
+        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+    return RTOPK_OK;
+}
+
+int rtopk_cache_load_fp8(const void *k_cache, const void *v_cache, const int64_t *cache_strides, const uint8_t *k_scales,
+                         const uint8_t *v_scales, int num_pages, int page, const int32_t *slots, int T, int Hkv, int D,
+                         void *k_out, void *v_out, int dtype, void *stream)
+{
+    const char *what = "8-bit cache load";
+    if (!k_out || !v_out || !slots || !k_cache || !v_cache || !k_scales || !v_scales)
+        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
+    rtopk::Cache8Args a{};
+    const int st = check_cache8(what, dtype, T, Hkv, D, cache_strides, num_pages, page, a);
+    if (st != RTOPK_OK)
+        return st;
+    if (k_out == v_out)
+        return set_error(RTOPK_EINVAL, "%s: keys and values need buffers of their own", what);
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.kc = (uint8_t *)k_cache;
+    a.vc = (uint8_t *)v_cache;
+    a.ksc = (uint8_t *)k_scales;
+    a.vsc = (uint8_t *)v_scales;
+    a.slots = slots;
+    bool wide = cache8_wide(a);
+    for (const void *p : {k_out, v_out}) {
+        if ((uintptr_t)p % (dtype == RTOPK_F32 ? 4 : 2))
+            return set_error(RTOPK_EINVAL, "%s: a pointer is not aligned to its element size", what);
+        wide = wide && (uintptr_t)p % 16 == 0;
+    }
+    const hipError_t e = rtopk::launch_cache8_load(a, dtype, wide, (hipStream_t)stream);
     if (e != hipSuccess)
         return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
     return RTOPK_OK;

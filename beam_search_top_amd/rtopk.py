@@ -105,6 +105,15 @@ def load():
     L.rtopk_cross_attention.restype = i32
     L.rtopk_cross_attention_workspace_bytes.argtypes = [i32] * 6
     L.rtopk_cross_attention_workspace_bytes.restype = sz
+    L.rtopk_qk_norm_rope.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, vp, vp, ctypes.c_float, i32, i32, i32, i32,
+                                     vp, vp, vp, vp, vp]
+    L.rtopk_qk_norm_rope.restype = i32
+    L.rtopk_cache_store_fp8.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp]
+    L.rtopk_cache_store_fp8.restype = i32
+    L.rtopk_cache_load_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, i32, vp]
+    L.rtopk_cache_load_fp8.restype = i32
+    L.rtopk_sample_filtered.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.rtopk_sample_filtered.restype = i32
     L.rtopk_read_probe.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
     L.rtopk_read_probe.restype = i32
     L.rtopk_read_probe_shape.argtypes = [vp, sz, i32, i32, ctypes.c_uint32, vp, vp]
@@ -317,6 +326,29 @@ def rtopk_cross_attention(q, q_strides, k, k_strides, v, v_strides, dtype, lens,
 
 def rtopk_cross_attention_workspace_bytes(B, N, S, Hq, Hkv, D):
     return load().rtopk_cross_attention_workspace_bytes(B, N, S, Hq, Hkv, D)
+
+
+def rtopk_qk_norm_rope(q, q_strides, k, k_strides, dtype, positions, freqs, rot, interleaved, q_weight, k_weight, eps, T,
+                       Hq, Hkv, D, q_out, q_out_strides, k_out, k_out_strides, stream):
+    return load().rtopk_qk_norm_rope(q, q_strides, k, k_strides, dtype, positions, freqs, rot, interleaved, q_weight,
+                                     k_weight, eps, T, Hq, Hkv, D, q_out, q_out_strides, k_out, k_out_strides, stream)
+
+
+def rtopk_cache_store_fp8(k, k_strides, v, v_strides, dtype, slots, T, Hkv, D, k_cache, v_cache, cache_strides, k_scales,
+                          v_scales, num_pages, page, stream):
+    return load().rtopk_cache_store_fp8(k, k_strides, v, v_strides, dtype, slots, T, Hkv, D, k_cache, v_cache,
+                                        cache_strides, k_scales, v_scales, num_pages, page, stream)
+
+
+def rtopk_cache_load_fp8(k_cache, v_cache, cache_strides, k_scales, v_scales, num_pages, page, slots, T, Hkv, D, k_out,
+                         v_out, dtype, stream):
+    return load().rtopk_cache_load_fp8(k_cache, v_cache, cache_strides, k_scales, v_scales, num_pages, page, slots, T, Hkv,
+                                       D, k_out, v_out, dtype, stream)
+
+
+def rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token, out_logprob, stream):
+    return load().rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token,
+                                        out_logprob, stream)
 
 
 def rtopk_read_probe(src, nbytes, marker, out, stream):
@@ -608,6 +640,175 @@ def cache_store(k, v, slots, k_cache, v_cache):
              _ints(slots, slots.shape, dev, "slots"), k.shape[0], Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(),
              _strides(k_cache, "k_cache"), pages, page)
     return k_cache, v_cache
+
+
+def _cache8(k_cache, v_cache, k_scales, v_scales, dev):
+    """The checks of an 8-bit cache: codes [pages, page, Hkv, D] and scales [pages, page, Hkv]."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must be [pages, page, Hkv, D] tensors of the same strides")
+    codes = (_torch.float8_e4m3fn, _torch.uint8)
+    if k_cache.dtype not in codes or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn or uint8")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.dtype is not _torch.uint8 or t.shape != shape[:3] or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 [pages, page, Hkv] tensor")
+    if not k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == dev:
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            _on_device(t, _torch.device("cuda", dev), name)
+    return shape
+
+
+def cache_store_fp8(k, v, slots, k_cache, v_cache, k_scales, v_scales):
+    """cache_store into a cache in 8 bits, quantising on the way.
+
+    k, v, slots as cache_store; k_cache, v_cache [pages, page, Hkv, D]
+    float8_e4m3fn (or uint8), k_scales, v_scales [pages, page, Hkv] uint8: the byte s
+    of a token's head stands for 2 ** (s - 127). Returns (k_cache, v_cache, k_scales, v_scales).
+    """
+    _get_torch()
+    if not k.is_cuda:
+        raise ValueError("k must be a device tensor")
+    dev = k.get_device()
+    if v.get_device() != dev:
+        _on_device(v, k.device, "v")
+    if k.dim() < 3 or k.shape != v.shape or k.dtype is not v.dtype:
+        raise ValueError("k and v must be [..., Hkv, D] tensors of one shape and type")
+    if slots.shape != k.shape[:-2]:
+        raise ValueError("slots must have the leading shape of k")
+    if k.dim() > 3:
+        k, v = (t.view(-1, *t.shape[-2:]) for t in (k, v))  # raises where the tokens are not evenly strided
+    pages, page, Hkv, D = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
+    if k.shape[1:] != (Hkv, D):
+        raise ValueError("k and v must have the cache's heads")
+    _enqueue(dev, load().rtopk_cache_store_fp8, k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), _code(k),
+             _ints(slots, slots.shape, dev, "slots"), k.shape[0], Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(),
+             _strides(k_cache, "k_cache"), k_scales.data_ptr(), v_scales.data_ptr(), pages, page)
+    return k_cache, v_cache, k_scales, v_scales
+
+
+def cache_load_fp8(k_cache, v_cache, k_scales, v_scales, slots, dtype=None, out=None):
+    """Reads tokens back out of a cache in 8 bits, on the current stream.
+
+    slots int32 of any shape (one outside the cache gives zeros; they may repeat).
+    Returns (k, v), each slots.shape + [Hkv, D] of `dtype` (None: bfloat16) or ``out``, which
+    may supply them.
+    """
+    torch = _get_torch()
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a device tensor")
+    dev = k_cache.get_device()
+    pages, page, Hkv, D = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
+    shape = slots.shape + (Hkv, D)
+    if out is None:
+        dtype = dtype or torch.bfloat16
+        k, v = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+    else:
+        if len(out) != 2:
+            raise ValueError("out must hold two tensors (k, v)")
+        k, v = out
+        if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or dtype not in (None, k.dtype) or \
+                not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError(f"out must be two contiguous {list(shape)} tensors of one type")
+        if not k.get_device() == v.get_device() == dev:
+            _on_device(k, k_cache.device, "out k")
+            _on_device(v, k_cache.device, "out v")
+    _enqueue(dev, load().rtopk_cache_load_fp8, k_cache.data_ptr(), v_cache.data_ptr(), _strides(k_cache, "k_cache"),
+             k_scales.data_ptr(), v_scales.data_ptr(), pages, page, _ints(slots, slots.shape, dev, "slots"), slots.numel(),
+             Hkv, D, k.data_ptr(), v.data_ptr(), _code(k))
+    return k, v
+
+
+def _rows3(t, name):
+    """t as [tokens, heads, D]; a view, so that writing to it writes to t."""
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be a [..., H, D] tensor")
+    return t if t.dim() == 3 else t.view(-1, *t.shape[-2:])  # raises where the tokens are not evenly strided
+
+
+def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None):
+    """Norms of queries and keys and their rotation by position, on the current stream.
+
+    q [..., Hq, D], k [..., Hkv, D] of one type (the leading dimensions, which must
+    be evenly strided, are the tokens), positions int32 of the leading shape (where negative, the
+    token's rows of the outputs stay as they were), freqs [rot / 2] float32 (radians per
+    position; rot <= D elements are rotated), q_weight, k_weight [D] (None: no norm). The outputs
+    may be supplied, q and k themselves among them; else they are new. Returns (q_out, k_out).
+    """
+    torch = _get_torch()
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    dev = q.get_device()
+    lead = q.shape[:-2]
+    if q.dim() < 3 or k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != q.shape[-1] or k.dtype is not q.dtype:
+        raise ValueError("q and k must be [..., Hq, D] and [..., Hkv, D] tensors of one type")
+    if freqs.dtype is not torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float32 [rot / 2] tensor")
+    if q_out is None:
+        # rows of skipped tokens have to hold something: zeros
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.zeros(k.shape, dtype=k.dtype, device=q.device)
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t.shape != like.shape or t.dtype is not q.dtype:
+            raise ValueError(f"{name} must have the shape and type of its input")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and (t.dtype is not q.dtype or t.shape != q.shape[-1:] or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [D] tensor of q's type")
+    for t, name in ((k, "k"), (freqs, "freqs"), (q_out, "q_out"), (k_out, "k_out"), (q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.get_device() != dev:
+            _on_device(t, q.device, name)
+    q3, k3, qo, ko = _rows3(q, "q"), _rows3(k, "k"), _rows3(q_out, "q_out"), _rows3(k_out, "k_out")
+    T, Hq, D = q3.shape
+    _enqueue(dev, load().rtopk_qk_norm_rope, q3.data_ptr(), _strides(q3, "q"), k3.data_ptr(), _strides(k3, "k"), _code(q),
+             _ints(positions, lead, dev, "positions"), freqs.data_ptr(), 2 * freqs.numel(), int(interleaved),
+             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps, T,
+             Hq, k3.shape[1], D, qo.data_ptr(), _strides(qo, "q_out"), ko.data_ptr(), _strides(ko, "k_out"))
+    return q_out, k_out
+
+
+def _row_values(t, R, dtype, dev, name):
+    """The address of a contiguous [R] tensor of this type on device number `dev`; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (R,) or not t.is_contiguous() or t.get_device() != dev:
+        _on_device(t, _torch.device("cuda", dev), name)
+        raise ValueError(f"{name} must be a contiguous {dtype} [{R}] tensor")
+    return t.data_ptr()
+
+
+def sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+    """Sampling of every row of logits [R, V] with filters, from given random numbers, on the current stream.
+
+    logits float32/float16/bfloat16, rows any distance apart; u [R] float32 in
+    [0, 1); temperature, top_p, min_p [R] float32 and top_k [R] int32, each None for none:
+    a row's k best, of those the shortest beginning with top_p of their weight, of those the ones with
+    min_p of the largest weight. ``out`` may supply the two results. Returns
+    (tokens [R] int32, logprobs [R] float32 under what is kept).
+    """
+    torch = _get_torch()
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a [R, V] device tensor")
+    dev = logits.get_device()
+    R, V = logits.shape
+    st = logits.stride()
+    if st[1] != 1 and V > 1:
+        raise ValueError("logits: the last dimension must be contiguous")
+    if out is None:
+        tok = torch.empty(R, dtype=torch.int32, device=logits.device)
+        lp = torch.empty(R, dtype=torch.float32, device=logits.device)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must hold two tensors (tokens, logprobs)")
+        tok, lp = out
+    f32 = torch.float32
+    _enqueue(dev, load().rtopk_sample_filtered, logits.data_ptr(), _code(logits), R, V, st[0],
+             _row_values(temperature, R, f32, dev, "temperature"), _row_values(top_k, R, torch.int32, dev, "top_k"),
+             _row_values(top_p, R, f32, dev, "top_p"), _row_values(min_p, R, f32, dev, "min_p"),
+             _row_values(u, R, f32, dev, "u"), _row_values(tok, R, torch.int32, dev, "out tokens"),
+             _row_values(lp, R, f32, dev, "out logprobs"))
+    return tok, lp
 
 
 def _attention_args(q, Hkv, scale, out, lse, workspace, dev):

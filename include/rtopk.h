@@ -489,6 +489,101 @@ int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k
 size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hkv, int D);
 
 /*
+ * The norms of queries and keys and their rotation by position, in one pass,
+ * in front of the store and the attention. Per head row x of D elements:
+ *     y_d = x_d / sqrt(mean(x^2) + eps) * w_d           (weight NULL: y = x)
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = positions[i] * freqs[j],
+ * for the pairs j < rot/2 of elements (j, j + rot/2), or (2j, 2j + 1) where
+ * interleaved; elements from rot on are not rotated.
+ *   q, k       device [T][Hq][D] and [T][Hkv][D], any of the three types;
+ *              q_strides, k_strides HOST [2] (token, head), as above
+ *   positions  device [T] int32 (rtopk_page_tables gives them); where negative, the
+ *              token's rows of both outputs stay as they were
+ *   freqs      device [rot/2] float32, radians per position (NULL when rot is 0)
+ *   rot        0 <= rot <= D, even; interleaved: 0 or not
+ *   q_weight, k_weight  device [D] in the type of q, each NULL for no norm
+ *   q_out, k_out  as q and k, with strides of their own, rows apart from each
+ *              other. An output may be its own input (the same address and strides);
+ *              otherwise it overlaps no input and no other output
+ * Norms and rotations are computed in float32, angles in float64; every output
+ * is rounded once. D <= 256, (Hq+Hkv)*D <= 2^20, T <= 2^28 (else RTOPK_ENOTSUP);
+ * eps finite, >= 0. Rows move as 16-byte vectors when D and rot are multiples of 32 bytes
+ * and all pointers and strides of 16, else element by element. Asynchronous on
+ * `stream`; one launch, no workspace.
+ */
+int rtopk_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, int dtype,
+                       const int32_t *positions, const float *freqs, int rot, int interleaved, const void *q_weight,
+                       const void *k_weight, float eps, int T, int Hq, int Hkv, int D, void *q_out,
+                       const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, void *stream);
+
+/*
+ * The paged cache in 8 bits. Codes are e4m3 (OCP: one sign, four exponent and
+ * three mantissa bits, largest 448, no infinity, NaN 0x7f and 0xff), one byte per
+ * element; every token has one scale byte s per head. Element = code * 2^(s - 127),
+ * with s held to [1, 254]. Half the bytes of a 16-bit cache.
+ *
+ * rtopk_cache_store_fp8 is rtopk_cache_store with quantising: the scale of a
+ * row of D elements is the smallest 2^e, e >= -126, with no finite element over
+ * 448 * 2^e; codes are rounded to nearest, ties to even. Elements over the largest value
+ * that the type of k holds in this form (float16 61440, else 240 * 2^120) are held to
+ * it. An infinity or NaN is stored as NaN and does not count for the scale. So
+ * an element is off by at most half a step: 2^-4 of itself, or 2^-17 of its row's
+ * largest where that is more (2^-136 where the scale is 2^-126).
+ *   k_cache, v_cache  device [num_pages][page][Hkv][D] bytes; cache_strides HOST
+ *              [3] (page, token, head) in bytes, the same for both
+ *   k_scales, v_scales  device [num_pages][page][Hkv] uint8, contiguous
+ *   dtype      type of k and v, any of the three; D <= 256 (else RTOPK_ENOTSUP)
+ * Everything else as rtopk_cache_store. Rows move 16 elements at a time when D is
+ * a multiple of 16 and pointers and strides of 16 bytes, else one by one.
+ */
+int rtopk_cache_store_fp8(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides, int dtype,
+                          const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache,
+                          const int64_t *cache_strides, uint8_t *k_scales, uint8_t *v_scales, int num_pages, int page,
+                          void *stream);
+
+/*
+ * Reads T tokens' keys and values back out of an 8-bit cache: k_out[t], v_out[t]
+ * are the elements at slot slots[t], rounded to `dtype` (exact for what
+ * rtopk_cache_store_fp8 has stored from that type or from a narrower one), and zeros
+ * where the slot is outside [0, num_pages*page). Slots may repeat.
+ *   k_out, v_out  device [T][Hkv][D] of type dtype, contiguous
+ * Asynchronous on `stream`; one launch, no workspace.
+ */
+int rtopk_cache_load_fp8(const void *k_cache, const void *v_cache, const int64_t *cache_strides, const uint8_t *k_scales,
+                         const uint8_t *v_scales, int num_pages, int page, const int32_t *slots, int T, int Hkv, int D,
+                         void *k_out, void *v_out, int dtype, void *stream);
+
+/*
+ * Sampling with temperature, top-k, top-p and min-p from given random numbers.
+ * Row r's candidates are its logits above -inf (a NaN counts as -inf), in order:
+ * larger logit first, equal ones by the lower token. With
+ * w_i = exp((x_i - max x) / temperature[r]) the row keeps
+ *   top_k[r] = k    the first k candidates (k <= 0 or k >= V: all), of those
+ *   top_p[r] = p    the shortest beginning, at least one, whose weights sum to at least
+ *                   p of theirs (p >= 1 or NaN: all), and of those
+ *   min_p[r] = m    the ones with w_i >= m (m held to [0, 1], NaN is 0).
+ * The token is the first kept one, in the order of tokens, at which the running sum
+ * of kept weights exceeds u[r] times their sum S; its log-probability is log(w_i / S).
+ * A temperature that is not above 0 keeps the first candidate alone. A row of no
+ * candidates gives token -1 and log-probability -inf. Where there are infinite
+ * logits, they weigh 1 and the others 0.
+ *   logits     device [R][V], any of the three types, rows ld >= V elements apart, any
+ *              base that is a multiple of the element size
+ *   temperature, top_p, min_p  device [R] float32, top_k device [R] int32, each NULL:
+ *              1, all, none, all
+ *   u          device [R] float32, held to [0, 1) (NaN is 0)
+ *   out_token  device [R] int32; out_logprob device [R] float32
+ * Weights are computed in 64 bits and summed as whole numbers of 2^-f, f = min(50,
+ * 62 - ceil(log2 V)), so that sums are exact and the same call gives the same result;
+ * a candidate of weight below 2^-(f+1) is never drawn. Logits as in rtopk_beam_step
+ * otherwise. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`;
+ * one launch, no workspace.
+ */
+int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                          int32_t *out_token, float *out_logprob, void *stream);
+
+/*
  * Measurement aid, not part of the selection: a plain streaming read that
  * gives the practical HBM ceiling the selection kernel is compared with. It
  * reads `bytes` bytes at `src` once with 16-byte non-temporal loads (ten per
