@@ -65,8 +65,10 @@ def _run(cmds, verbose):
 def build(verbose: bool = False, extra=()) -> str:
     tag = f".tmp{os.getpid()}"
     objs = [LIB + f".dt{d}{tag}.o" for d in DTYPES] + [LIB + f".{n}{tag}.o" for n in (
-        "rope", "cache8", "filter", "filterhost", "attn", "paged", "layer", "noalloc", "sample", "reorder", "host")]
+        "attn8", "rope", "cache8", "filter", "filterhost", "attn", "paged", "layer", "noalloc", "sample", "reorder", "host")]
     cmds = [[HIPCC, *FLAGS, *extra, f"-DRTOPK_DTYPE={d}", "-c", KERNELS, "-o", o] for d, o in zip(DTYPES, objs)]
+    # the attention kernels once more, for caches in 8 bits
+    cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-DRTOPK_ATTN_F8", "-c", ATTN, "-o", objs[-12]])
     cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", ROPE, "-o", objs[-11]])
     cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", CACHE8, "-o", objs[-10]])
     cmds.append([HIPCC, *ATTN_FLAGS, *extra, "-c", FILTER, "-o", objs[-9]])

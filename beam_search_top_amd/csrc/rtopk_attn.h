@@ -70,6 +70,11 @@ struct AttnArgs {
     uint32_t *ticket;          // [B * Hkv] arrivals of attn_few's shares, zero between calls
 };
 
+// The same over a cache in 8 bits (a tree).
+struct AttnArgs8 : AttnArgs {
+    const uint8_t *ksc, *vsc; // scales [num_pages][page][Hkv]
+};
+
 // How a call is cut: workgroups of `waves` x 32 rows (few: of 16 or 32 rows,
 // by attn_few), tiles of `bn` keys, heads padded to `dp` elements, keys in at
 // most `nsplit` parts of at least min_tiles tiles (attn_few: in `units` shares).
@@ -81,6 +86,7 @@ struct AttnPlan {
 // wide: rows of keys or values lie 2^25 elements or more apart (not for attn_few)
 AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide);
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s);
+hipError_t launch_attention_fp8(const AttnArgs8 &a, const AttnPlan &p, int dtype, hipStream_t s); // a tree
 
 // Calls `launch` with a library-owned workspace of `need` bytes for `stream`
 // (rtopk_host.cpp), held until it returns; a status code.

@@ -7,10 +7,29 @@
 // a row that may see no key gives o = 0 and lse = -inf.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "rtopk_attn.h"
+#include "rtopk_cache8.h"
 
 namespace rtopk {
 namespace {
+
+// This source is compiled twice: for caches of the type of q, and (RTOPK_ATTN_F8)
+// for caches of e4m3 codes with a power of two per token and head (rtopk_cache8.h), whose
+// elements become numbers of the type of q on their way into LDS or into operands.
+#ifdef RTOPK_ATTN_F8
+constexpr bool kF8 = true;
+typedef AttnArgs8 Args;
+#else
+constexpr bool kF8 = false;
+typedef AttnArgs Args;
+#endif
+__device__ __forceinline__ const uint8_t *k_scales(const AttnArgs8 &a) { return a.ksc; }
+__device__ __forceinline__ const uint8_t *v_scales(const AttnArgs8 &a) { return a.vsc; }
+__device__ __forceinline__ const uint8_t *k_scales(const AttnArgs &) { return nullptr; }
+__device__ __forceinline__ const uint8_t *v_scales(const AttnArgs &) { return nullptr; }
+constexpr int kElemBytes = kF8 ? 1 : 2; // of a cache's element
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -38,6 +57,11 @@ template <> struct Elem<1> {
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
+    // two of four codes times a power of two (HI: the upper two)
+    template <bool HI> static __device__ __forceinline__ uint32_t decoded(uint32_t codes, float by)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)codes, by, HI));
+    }
 };
 template <> struct Elem<2> {
     typedef __bf16 T;
@@ -48,6 +72,10 @@ template <> struct Elem<2> {
     static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    template <bool HI> static __device__ __forceinline__ uint32_t decoded(uint32_t codes, float by)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)codes, by, HI));
     }
 };
 
@@ -158,6 +186,15 @@ template <typename E> __device__ __forceinline__ float row_lse(float m, float l)
     return l == 0.f ? -INFINITY : (m + E::kBelow + __builtin_log2f(E::kBelow == 0.f ? l : l * (1.f / (1 << (int)E::kBelow)))) * kLn2;
 }
 
+// 2^(s - 127) of a scale byte
+__device__ __forceinline__ float power_of(uint32_t s) { return __uint_as_float(scale_bits(held_scale(s))); }
+
+// One element of an 8-bit cache in the type of q
+template <typename E> __device__ __forceinline__ typename E::T element8(uint8_t code, uint8_t scale)
+{
+    return __builtin_bit_cast(typename E::V2, E::template decoded<false>(code, power_of(scale)))[0];
+}
+
 // Tiles in each ring: as many as the LDS of a CU holds for one workgroup of
 // eight waves, or two for each of two workgroups of four.
 constexpr int ring_tiles(int wr) { return wr == 8 ? 4 : 2; }
@@ -175,6 +212,16 @@ template <int N> __device__ __forceinline__ void ring_wait(bool full)
         __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14)); // vmcnt(N) lgkmcnt(0)
     else
         __builtin_amdgcn_s_waitcnt(0x0070); // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Wait until this wave's LDS reads and writes are done, then meet the other waves
+// (loads to registers stay in flight).
+__device__ __forceinline__ void lds_wait()
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
@@ -205,7 +252,7 @@ __device__ __forceinline__ void values_operand(V8 (&v)[DB], const int (&at)[DB],
 }
 
 template <int DT, int DP, int WR, bool TREE>
-__global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) void attn_tiles(const AttnArgs a)
+__global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) void attn_tiles(const Args a)
 {
     typedef Elem<DT> E;
     typedef typename E::T T;
@@ -217,7 +264,8 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
     constexpr int RPL = 1024 / ROWB;                  // rows of one 1 KiB load of a wave
     constexpr int NI = BN / RPL / WR > 0 ? BN / RPL / WR : 1; // loads per wave and tensor
     static_assert(BN % (RPL * WR) == 0, "a tile is whole loads of every wave");
-    constexpr int ST = ring_tiles(WR);
+    constexpr int ST = kF8 ? 2 : ring_tiles(WR);
+    constexpr int AHEAD = kF8 ? ST + 1 : ST; // tiles from this one to the last whose keys are on their way
     constexpr int kWords = kMaxTree / 64;
     __shared__ __align__(1024) uint8_t smem[2 * ST * TILEB]; // a ring of K tiles, a ring of V tiles
     __shared__ uint64_t s_up[TREE ? kMaxTree * kWords : 1]; // ancestors of every node
@@ -360,8 +408,8 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
 
     // ---- loads. Lane l of a wave's load i brings slot l mod CH of row
     // (wave * NI + i) * RPL + l / CH
-    const char *kbase = static_cast<const char *>(a.k) + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
-    const char *vbase = static_cast<const char *>(a.v) + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
+    const char *kbase = static_cast<const char *>(a.k) + kElemBytes * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
+    const char *vbase = static_cast<const char *>(a.v) + kElemBytes * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
     const int lrow = lane / CH, lslot = lane % CH;
     // What decides about a key, its page or its mask, for a window of keys that
     // is read ahead now and then: lane l holds the page id of page win + l, or
@@ -395,9 +443,10 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
     struct Tile {
         uint64_t oks; // the keys that count, one bit each
         int64_t off;  // tree: byte offset of this lane's key, -1: does not count
+        int slot;     // 8 bits: its slot
     };
     auto place = [&](int t) -> Tile {
-        Tile p{0, -1};
+        Tile p{0, -1, 0};
         if (t >= t_end)
             return p;
         refill(t);
@@ -407,7 +456,8 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
             const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : t * BN));
             const int id = checked_page(__shfl(held, pg - win), a.num_pages);
             ok = ok && id >= 0;
-            p.off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
+            p.off = ok ? kElemBytes * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : -1;
+            p.slot = ok ? id * (int)a.page.d + (j - pg * (int)a.page.d) : 0;
         } else if (a.key_mask) {
             const int w = t * BN + lane - win, out = __shfl(held, (w >> 3) & 63) >> (w & 7) & 1; // for every lane: none may be idle
             ok = ok && !out;
@@ -458,6 +508,55 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
         }
     };
 
+    // ---- loads of an 8-bit cache: to registers, a lane 16 codes of one key, a wave 1 KiB
+    // a load; a step later they go to LDS as numbers of the type of q, 2 chunks each.
+    constexpr int CH8 = DP / 16, RPL8 = 64 / CH8, NI8 = BN / RPL8 / WR > 0 ? BN / RPL8 / WR : 1;
+    struct Codes {
+        u32x4 c[NI8];
+        uint32_t s; // the scale of this lane's key
+    };
+    const int lrow8 = lane / CH8, lch8 = lane % CH8;
+    // rows of a load lie evenly on one page
+    const bool even8 = a.page.d % RPL8 == 0 && a.ks[1] < (1 << 25);
+    auto fetch8 = [&](const Tile &p, const char *base, const uint8_t *scales, Codes &to) {
+        to.s = scales[(int64_t)p.slot * a.Hkv + hk]; // of a key that does not count: of slot 0
+        const bool whole8 = even8 && p.oks == (BN == 64 ? ~0ull : (1ull << BN) - 1);
+#pragma unroll
+        for (int i = 0; i < NI8; ++i) {
+            const int lr = (wave * NI8 + i) * RPL8, r = (lr + lrow8) & (BN - 1);
+            int64_t at;
+            if (whole8) {
+                const int from = lr & (BN - 1);
+                at = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(p.off >> 32), from) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)p.off, from)) + lrow8 * (uint32_t)a.ks[1];
+            } else {
+                at = ((int64_t)__shfl((int)(p.off >> 32), r) << 32) | (uint32_t)__shfl((int)p.off, r);
+                at = at < 0 ? 0 : at; // some place that can be read; not used
+            }
+            to.c[i] = *(gu32x4 *)(base + at + (lch8 * 16 < a.D ? lch8 * 16 : 0));
+        }
+    };
+    auto put8 = [&](const Codes &from, uint64_t counts, bool values, uint8_t *to) {
+#pragma unroll
+        for (int i = 0; i < NI8; ++i) {
+            const int lr = (wave * NI8 + i) * RPL8, r = (lr + lrow8) & (BN - 1);
+            const float by = power_of((uint32_t)__shfl((int)from.s, r));
+            const bool in = (counts >> r & 1) && lch8 * 16 < a.D;
+            u32x4 y[2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t lo = E::template decoded<false>(from.c[i][x], by), hi = E::template decoded<true>(from.c[i][x], by);
+                y[x / 2][x % 2 * 2] = in ? lo : 0u;
+                y[x / 2][x % 2 * 2 + 1] = in ? hi : 0u;
+            }
+            const int f = values ? fv<CH>(r) : fk<CH>(r);
+            if (lr < BN) { // the same for the wave: with eight waves and heads of 64, half of them bring a tile
+                *reinterpret_cast<u32x4 *>(to + r * ROWB + ((2 * lch8) ^ f) * 16) = y[0];
+                *reinterpret_cast<u32x4 *>(to + r * ROWB + ((2 * lch8 + 1) ^ f) * 16) = y[1];
+            }
+        }
+    };
+
     f32x16 o[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -490,23 +589,46 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
     // while the weights of tile t are computed, so that a wave keeps the matrix
     // cores and the vector unit busy at once.
     f32x16 x0[KB], x1[KB]; // scores of this tile and the next, in turn
-    uint64_t oks[ST + 1];  // of tiles t, t + 1, ...
-    Tile last{0, -1};      // the last tile whose keys are on their way
+    uint64_t oks[AHEAD + 1]; // of tiles t, t + 1, ...
+    Tile last{0, -1, 0};     // the last tile whose keys are on their way
 #pragma unroll
-    for (int i = 0; i <= ST; ++i)
+    for (int i = 0; i <= AHEAD; ++i)
         oks[i] = 0;
+    Codes kq, vq; // 8 bits: of keys t + 2 and values t + 1
+    if constexpr (kF8) {
+        const Tile p0 = place(t_begin), p1 = place(t_begin + 1);
+        last = place(t_begin + 2);
+        oks[0] = p0.oks;
+        oks[1] = p1.oks;
+        oks[2] = last.oks;
+        if (t_begin < t_end) {
+            Codes k1, v0;
+            fetch8(p0, kbase, k_scales(a), kq);
+            fetch8(p1, kbase, k_scales(a), k1);
+            fetch8(p0, vbase, v_scales(a), v0);
+            put8(kq, oks[0], false, kbuf);
+            fetch8(last, kbase, k_scales(a), kq);
+            put8(k1, oks[1], false, kbuf + TILEB);
+            fetch8(p1, vbase, v_scales(a), vq);
+            put8(v0, oks[0], true, vbuf);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < ST; ++i) { // keys 0; keys 1, values 0; keys 2, values 1; ...
-        const Tile p = place(t_begin + i);
-        oks[i] = p.oks;
-        if (t_begin + i < t_end)
-            load_tile(p, t_begin + i, kbase, a.ks[1], false, kbuf + i * TILEB);
-        if (i > 0 && t_begin + i - 1 < t_end)
-            load_tile(last, t_begin + i - 1, vbase, a.vs[1], true, vbuf + (i - 1) * TILEB);
-        last = p;
+        for (int i = 0; i < ST; ++i) { // keys 0; keys 1, values 0; keys 2, values 1; ...
+            const Tile p = place(t_begin + i);
+            oks[i] = p.oks;
+            if (t_begin + i < t_end)
+                load_tile(p, t_begin + i, kbase, a.ks[1], false, kbuf + i * TILEB);
+            if (i > 0 && t_begin + i - 1 < t_end)
+                load_tile(last, t_begin + i - 1, vbase, a.vs[1], true, vbuf + (i - 1) * TILEB);
+            last = p;
+        }
     }
     if (t_begin < t_end) {
-        ring_wait<2 * (ST - 1) * NI>(t_begin + ST <= t_end);
+        if constexpr (kF8)
+            lds_wait();
+        else
+            ring_wait<2 * (ST - 1) * NI>(t_begin + ST <= t_end);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
             x0[k] = scores(kbuf, k);
@@ -514,13 +636,23 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
     auto step = [&](int t, f32x16 (&x)[KB], f32x16 (&y)[KB]) {
         // keys t + 1 and values t are in LDS; every wave is done with keys t and values t - 1
         const int at = (t - t_begin) & (ST - 1);
-        ring_wait<2 * (ST - 2) * NI>(t + ST <= t_end);
-        if (t + ST - 1 < t_end)
-            load_tile(last, t + ST - 1, vbase, a.vs[1], true, vbuf + ((at + ST - 1) & (ST - 1)) * TILEB);
-        last = place(t + ST);
-        if (t + ST < t_end)
-            load_tile(last, t + ST, kbase, a.ks[1], false, kbuf + at * TILEB);
-        oks[ST] = last.oks;
+        if constexpr (kF8) {
+            // what was loaded a step ago goes to LDS, and the next loads start
+            lds_wait();
+            put8(vq, oks[1], true, vbuf + (at ^ 1) * TILEB);
+            fetch8(last, vbase, v_scales(a), vq);
+            put8(kq, oks[2], false, kbuf + at * TILEB);
+            last = place(t + AHEAD);
+            fetch8(last, kbase, k_scales(a), kq);
+        } else {
+            ring_wait<2 * (ST - 2) * NI>(t + ST <= t_end);
+            if (t + ST - 1 < t_end)
+                load_tile(last, t + ST - 1, vbase, a.vs[1], true, vbuf + ((at + ST - 1) & (ST - 1)) * TILEB);
+            last = place(t + ST);
+            if (t + ST < t_end)
+                load_tile(last, t + ST, kbase, a.ks[1], false, kbuf + at * TILEB);
+        }
+        oks[AHEAD] = last.oks;
         const uint8_t *ks = kbuf + ((at + 1) & (ST - 1)) * TILEB, *vs = vbuf + at * TILEB;
 
         const bool in_tree = walk && (t + 1) * BN > kr.tree0;
@@ -636,7 +768,7 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
                 o[d] = E::mfma(vf[n % 2][d], p[n / 2][n % 2], o[d]);
         }
 #pragma unroll
-        for (int i = 0; i < ST; ++i)
+        for (int i = 0; i < AHEAD; ++i)
             oks[i] = oks[i + 1];
     };
     int t = t_begin;
@@ -659,16 +791,27 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
                     continue;
                 const int pos = (tree_tile + w) * BN + j, pg = (int)page_of(a.page, (uint32_t)pos);
                 const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
-                const T *vr = reinterpret_cast<const T *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+                // (8 bits: the codes' row and its scale)
+                typedef std::conditional_t<kF8, uint8_t, T> C;
+                const C *vr = reinterpret_cast<const C *>(vbase) + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+                uint8_t scale = 0;
+                if constexpr (kF8)
+                    scale = v_scales(a)[((int64_t)id * (int)a.page.d + (pos - pg * (int)a.page.d)) * a.Hkv + hk];
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
                         if (e < a.D) {
-                            const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
-                            if ((raw & E::kExp) == E::kExp)
-                                o[d][i] += (float)vr[e];
+                            if constexpr (kF8) {
+                                const T x = element8<E>(vr[e], scale);
+                                if ((__builtin_bit_cast(uint16_t, x) & E::kExp) == E::kExp)
+                                    o[d][i] += (float)x;
+                            } else {
+                                const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
+                                if ((raw & E::kExp) == E::kExp)
+                                    o[d][i] += (float)vr[e];
+                            }
                         }
                     }
             }
@@ -858,7 +1001,7 @@ template <bool TREE> __device__ __forceinline__ Share find_share(const AttnArgs 
 // (Modes of one kernel, not branches in it: the counts by which a wave waits for
 // its older loads only must be the same on every path.)
 template <int DT, int DP, int NB, int MODE>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
 {
     constexpr bool TREE = MODE != 0;
     typedef Elem<DT> E;
@@ -1328,7 +1471,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const AttnArgs a)
 
 // Joins the splits of attn_tiles, in their order: a wave per row, eight parts'
 // loads in flight (4060 rows of 80, nine parts: 6.8 us; one part at a time 11.6).
-template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int bn)
+template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn_join(const Args a, int bn)
 {
     typedef typename Elem<DT>::T T;
     const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -1385,10 +1528,10 @@ template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn
         a.lse[at] = row_lse<Elem<DT>>(M, L);
 }
 
-template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+template <int DT, int DP, bool TREE> hipError_t launch_dims(const Args &a, const AttnPlan &p, hipStream_t s)
 {
     const dim3 grid((unsigned)p.grid);
-    if constexpr (DP <= 128) {
+    if constexpr (DP <= 128 && !kF8) {
         if (p.few) {
             const dim3 block(64 * kFewWaves);
             if constexpr (TREE) {
@@ -1426,7 +1569,7 @@ template <int DT, int DP, bool TREE> hipError_t launch_dims(const AttnArgs &a, c
     return e;
 }
 
-template <int DT, bool TREE> hipError_t launch_type(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+template <int DT, bool TREE> hipError_t launch_type(const Args &a, const AttnPlan &p, hipStream_t s)
 {
     if (p.dp == 64)
         return launch_dims<DT, 64, TREE>(a, p, s);
@@ -1437,11 +1580,18 @@ template <int DT, bool TREE> hipError_t launch_type(const AttnArgs &a, const Att
 
 } // namespace
 
-hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s)
+#ifdef RTOPK_ATTN_F8
+hipError_t launch_attention_fp8(const Args &a, const AttnPlan &p, int dtype, hipStream_t s)
+{
+    return dtype == 1 ? launch_type<1, true>(a, p, s) : launch_type<2, true>(a, p, s);
+}
+#else
+hipError_t launch_attention(const Args &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s)
 {
     if (dtype == 1)
         return tree ? launch_type<1, true>(a, p, s) : launch_type<1, false>(a, p, s);
     return tree ? launch_type<2, true>(a, p, s) : launch_type<2, false>(a, p, s);
 }
+#endif
 
 } // namespace rtopk

@@ -42,9 +42,10 @@ bool strides_fit(const int64_t st[3], long long n0, long long n1, long long n2)
     return sum <= most;
 }
 
-// A [n0][n1][n2][D] view that is read 16 bytes at a time. The stride of a
+// A [n0][n1][n2][D] view that is read 16 bytes (`unit` elements) at a time. The stride of a
 // dimension of one entry says nothing and is dropped.
-int check_view(const char *what, const char *name, const void *p, int64_t st[3], long long n0, long long n1, long long n2)
+int check_view(const char *what, const char *name, const void *p, int64_t st[3], long long n0, long long n1, long long n2,
+               int unit = 8)
 {
     const long long n[3] = {n0, n1, n2};
     for (int i = 0; i < 3; ++i)
@@ -52,9 +53,9 @@ int check_view(const char *what, const char *name, const void *p, int64_t st[3],
     if ((uintptr_t)p % 16)
         return set_error(RTOPK_EINVAL, "%s: %s is not 16-byte aligned", what, name);
     for (int i = 0; i < 3; ++i)
-        if (st[i] % 8)
-            return set_error(RTOPK_EINVAL, "%s: %s stride %lld is not a multiple of 8 elements", what, name,
-                             (long long)st[i]);
+        if (st[i] % unit)
+            return set_error(RTOPK_EINVAL, "%s: %s stride %lld is not a multiple of %d elements", what, name,
+                             (long long)st[i], unit);
     if (!strides_fit(st, n0, n1, n2))
         return set_error(RTOPK_EINVAL, "%s: %s strides are negative or overflow", what, name);
     return RTOPK_OK;
@@ -138,11 +139,11 @@ size_t attention_bytes(int B, int N, int Hq, int Hkv, int D, int S)
     return x > y ? x : y;
 }
 
-int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree, void *workspace, size_t ws_bytes,
+int enqueue_attention(const char *what, rtopk::AttnArgs8 &a, int dtype, bool tree, bool fp8, void *workspace, size_t ws_bytes,
                       hipStream_t stream)
 {
     // attn_few holds the offsets of 32 rows in 32 bits, and needs 32 rows to read
-    const bool wide = a.ks[1] >= (1 << 25) || a.vs[1] >= (1 << 25) || (!tree && a.S < 32);
+    const bool wide = fp8 || a.ks[1] >= (1 << 25) || a.vs[1] >= (1 << 25) || (!tree && a.S < 32);
     const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S, wide);
     if (workspace && (uintptr_t)workspace % 256)
         return set_error(RTOPK_EINVAL, "%s: workspace is not 256-byte aligned", what);
@@ -161,7 +162,8 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
         a.ml = ws ? (float *)((uint8_t *)ws + p.ml_off) : nullptr;
         a.part = ws ? (float *)((uint8_t *)ws + p.part_off) : nullptr;
         a.ticket = ws ? (uint32_t *)((uint8_t *)ws + rtopk::kWsTicketOff) : nullptr;
-        const hipError_t e = rtopk::launch_attention(a, p, dtype, tree, stream);
+        const hipError_t e = fp8 ? rtopk::launch_attention_fp8(a, p, dtype, stream)
+                                 : rtopk::launch_attention(a, p, dtype, tree, stream);
         if (e != hipSuccess)
             return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
         return (int)RTOPK_OK;
@@ -169,6 +171,63 @@ int enqueue_attention(const char *what, rtopk::AttnArgs &a, int dtype, bool tree
     if (p.ws_bytes == rtopk::kWsFixedBytes || workspace)
         return go(workspace);
     return rtopk::with_workspace(p.ws_bytes, stream, go);
+}
+
+// Tree attention over a cache of the type of q or (fp8) of 8 bits.
+int tree_attention(const char *what, bool fp8, const void *q, const int64_t *q_strides, const void *k_cache,
+                   const void *v_cache, const int64_t *cache_strides, const uint8_t *k_scales, const uint8_t *v_scales,
+                   int dtype, const int32_t *table, int table_ld, int num_pages, int page, const int32_t *cache_lens,
+                   const int32_t *parents, const int32_t *sizes, int B, int N, int Hq, int Hkv, int D, float scale, void *out,
+                   float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (!q || !k_cache || !v_cache || !table || !cache_lens || !out || (fp8 && (!k_scales || !v_scales)))
+        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
+    int st = check_attention(what, dtype, B, N, Hq, Hkv, D, scale);
+    if (st != RTOPK_OK)
+        return st;
+    if (table_ld < 1 || num_pages < 1 || page < 1)
+        return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (table_ld=%d num_pages=%d page=%d)", what, table_ld,
+                         num_pages, page);
+    if (!mul_fits(num_pages, page, INT_MAX) || !mul_fits(table_ld, page, INT_MAX - 4096))
+        return set_error(RTOPK_EINVAL, "%s: num_pages*page or table_ld*page exceeds 2^31-4097", what);
+    if (N > rtopk::kMaxTree)
+        return set_error(RTOPK_ENOTSUP, "%s: N=%d exceeds the implementation limit %d", what, N, rtopk::kMaxTree);
+    if (fp8 && D % 16)
+        return set_error(RTOPK_ENOTSUP, "%s: D=%d is not a multiple of 16", what, D);
+    const int unit = fp8 ? 16 : 8; // elements of a cache's 16 bytes
+    rtopk::AttnArgs8 a{};
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    set_strides(a.qs, q_strides, N, Hq, D);
+    set_strides(a.ks, cache_strides, page, Hkv, D);
+    set_strides(a.vs, cache_strides, page, Hkv, D);
+    if ((st = check_view(what, "q", q, a.qs, B, N, Hq)) != RTOPK_OK ||
+        (st = check_view(what, "k_cache", k_cache, a.ks, num_pages, page, Hkv, unit)) != RTOPK_OK ||
+        (st = check_view(what, "v_cache", v_cache, a.vs, num_pages, page, Hkv, unit)) != RTOPK_OK)
+        return st;
+    if ((uintptr_t)out % 16)
+        return set_error(RTOPK_EINVAL, "%s: out is not 16-byte aligned", what);
+    a.B = B;
+    a.N = N;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.D = D;
+    a.S = table_ld * page;
+    a.scale = scale;
+    a.lens = cache_lens;
+    a.table = table;
+    a.ld = table_ld;
+    a.num_pages = num_pages;
+    a.ksc = k_scales;
+    a.vsc = v_scales;
+    a.page = rtopk::make_page_div((uint32_t)page);
+    a.parents = parents;
+    a.sizes = sizes;
+    a.out = out;
+    a.lse = lse;
+    return guarded(what, [&] { return enqueue_attention(what, a, dtype, true, fp8, workspace, ws_bytes, (hipStream_t)stream); });
 }
 
 } // namespace
@@ -484,50 +543,20 @@ int rtopk_tree_attention(const void *q, const int64_t *q_strides, const void *k_
                          int Hq, int Hkv, int D, float scale, void *out, float *lse, void *workspace, size_t ws_bytes,
                          void *stream)
 {
-    const char *what = "tree attention";
-    if (!q || !k_cache || !v_cache || !table || !cache_lens || !out)
-        return set_error(RTOPK_EINVAL, "%s: NULL pointer", what);
-    int st = check_attention(what, dtype, B, N, Hq, Hkv, D, scale);
-    if (st != RTOPK_OK)
-        return st;
-    if (table_ld < 1 || num_pages < 1 || page < 1)
-        return set_error(RTOPK_EINVAL, "%s: sizes must be >= 1 (table_ld=%d num_pages=%d page=%d)", what, table_ld,
-                         num_pages, page);
-    if (!mul_fits(num_pages, page, INT_MAX) || !mul_fits(table_ld, page, INT_MAX - 4096))
-        return set_error(RTOPK_EINVAL, "%s: num_pages*page or table_ld*page exceeds 2^31-4097", what);
-    if (N > rtopk::kMaxTree)
-        return set_error(RTOPK_ENOTSUP, "%s: N=%d exceeds the implementation limit %d", what, N, rtopk::kMaxTree);
-    rtopk::AttnArgs a{};
-    a.q = q;
-    a.k = k_cache;
-    a.v = v_cache;
-    set_strides(a.qs, q_strides, N, Hq, D);
-    set_strides(a.ks, cache_strides, page, Hkv, D);
-    set_strides(a.vs, cache_strides, page, Hkv, D);
-    if ((st = check_view(what, "q", q, a.qs, B, N, Hq)) != RTOPK_OK ||
-        (st = check_view(what, "k_cache", k_cache, a.ks, num_pages, page, Hkv)) != RTOPK_OK ||
-        (st = check_view(what, "v_cache", v_cache, a.vs, num_pages, page, Hkv)) != RTOPK_OK)
-        return st;
-    if ((uintptr_t)out % 16)
-        return set_error(RTOPK_EINVAL, "%s: out is not 16-byte aligned", what);
-    a.B = B;
-    a.N = N;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.G = Hq / Hkv;
-    a.D = D;
-    a.S = table_ld * page;
-    a.scale = scale;
-    a.lens = cache_lens;
-    a.table = table;
-    a.ld = table_ld;
-    a.num_pages = num_pages;
-    a.page = rtopk::make_page_div((uint32_t)page);
-    a.parents = parents;
-    a.sizes = sizes;
-    a.out = out;
-    a.lse = lse;
-    return guarded(what, [&] { return enqueue_attention(what, a, dtype, true, workspace, ws_bytes, (hipStream_t)stream); });
+    return tree_attention("tree attention", false, q, q_strides, k_cache, v_cache, cache_strides, nullptr, nullptr, dtype,
+                          table, table_ld, num_pages, page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale, out, lse,
+                          workspace, ws_bytes, stream);
+}
+
+int rtopk_tree_attention_fp8(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
+                             const int64_t *cache_strides, const uint8_t *k_scales, const uint8_t *v_scales, int dtype,
+                             const int32_t *table, int table_ld, int num_pages, int page, const int32_t *cache_lens,
+                             const int32_t *parents, const int32_t *sizes, int B, int N, int Hq, int Hkv, int D, float scale,
+                             void *out, float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    return tree_attention("8-bit tree attention", true, q, q_strides, k_cache, v_cache, cache_strides, k_scales, v_scales,
+                          dtype, table, table_ld, num_pages, page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale, out,
+                          lse, workspace, ws_bytes, stream);
 }
 
 size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int table_ld, int page)
@@ -560,7 +589,7 @@ int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k
         return set_error(RTOPK_EINVAL, "%s: S=%d must be >= 1", what, S);
     if (S > INT_MAX - 4096)
         return set_error(RTOPK_ENOTSUP, "%s: S=%d exceeds 2^31-4097", what, S);
-    rtopk::AttnArgs a{};
+    rtopk::AttnArgs8 a{};
     a.q = q;
     a.k = k;
     a.v = v;
@@ -586,7 +615,7 @@ int rtopk_cross_attention(const void *q, const int64_t *q_strides, const void *k
     a.page = rtopk::make_page_div(1);
     a.out = out;
     a.lse = lse;
-    return guarded(what, [&] { return enqueue_attention(what, a, dtype, false, workspace, ws_bytes, (hipStream_t)stream); });
+    return guarded(what, [&] { return enqueue_attention(what, a, dtype, false, false, workspace, ws_bytes, (hipStream_t)stream); });
 }
 
 } // extern "C"

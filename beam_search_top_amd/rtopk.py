@@ -112,6 +112,9 @@ def load():
     L.rtopk_cache_store_fp8.restype = i32
     L.rtopk_cache_load_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, i32, vp]
     L.rtopk_cache_load_fp8.restype = i32
+    L.rtopk_tree_attention_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, i32, i32, i32,
+                                           i32, i32, ctypes.c_float, vp, vp, vp, sz, vp]
+    L.rtopk_tree_attention_fp8.restype = i32
     L.rtopk_sample_filtered.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp]
     L.rtopk_sample_filtered.restype = i32
     L.rtopk_read_probe.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
@@ -344,6 +347,14 @@ def rtopk_cache_load_fp8(k_cache, v_cache, cache_strides, k_scales, v_scales, nu
                          v_out, dtype, stream):
     return load().rtopk_cache_load_fp8(k_cache, v_cache, cache_strides, k_scales, v_scales, num_pages, page, slots, T, Hkv,
                                        D, k_out, v_out, dtype, stream)
+
+
+def rtopk_tree_attention_fp8(q, q_strides, k_cache, v_cache, cache_strides, k_scales, v_scales, dtype, table, table_ld,
+                             num_pages, page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale, out, lse, workspace,
+                             ws_bytes, stream):
+    return load().rtopk_tree_attention_fp8(q, q_strides, k_cache, v_cache, cache_strides, k_scales, v_scales, dtype, table,
+                                           table_ld, num_pages, page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale,
+                                           out, lse, workspace, ws_bytes, stream)
 
 
 def rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token, out_logprob, stream):
@@ -859,6 +870,29 @@ def tree_attention(q, k_cache, v_cache, table, cache_lens, parents=None, sizes=N
     _enqueue(dev, load().rtopk_tree_attention, q.data_ptr(), _strides(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
              _strides(k_cache, "k_cache"), _code(q), _ints(table, (B, ld), dev, "table"), ld, pages, page,
              _ints(cache_lens, (B,), dev, "cache_lens"), None if parents is None else _ints(parents, (B, N), dev, "parents"),
+             None if sizes is None else _ints(sizes, (B,), dev, "sizes"), B, N, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
+    return out, lse
+
+
+def tree_attention_fp8(q, k_cache, v_cache, k_scales, v_scales, table, cache_lens, parents=None, sizes=None, scale=None,
+                       out=None, lse=None, workspace=None):
+    """tree_attention over a cache in 8 bits, as cache_store_fp8 fills it: k_cache, v_cache
+    [pages, page, Hkv, D] float8_e4m3fn (or uint8), D a multiple of 16, and k_scales, v_scales
+    [pages, page, Hkv] uint8; everything else as tree_attention. Returns (out, lse)."""
+    _get_torch()
+    if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
+        raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")
+    dev = q.get_device()
+    B, N, Hq, D = q.shape
+    pages, page, Hkv, Dk = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
+    if Dk != D:
+        raise ValueError("the cache must have q's head size")
+    ld = table.shape[1]
+    scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
+    _enqueue(dev, load().rtopk_tree_attention_fp8, q.data_ptr(), _strides(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
+             _strides(k_cache, "k_cache"), k_scales.data_ptr(), v_scales.data_ptr(), _code(q),
+             _ints(table, (B, ld), dev, "table"), ld, pages, page, _ints(cache_lens, (B,), dev, "cache_lens"),
+             None if parents is None else _ints(parents, (B, N), dev, "parents"),
              None if sizes is None else _ints(sizes, (B,), dev, "sizes"), B, N, Hq, Hkv, D, scale, out.data_ptr(), lp, wp, wn)
     return out, lse
 

@@ -172,3 +172,23 @@ def test_host_tensors_are_refused(lib):
         rtopk.cache_load_fp8(torch.zeros(2, 4, 2, 64, dtype=torch.uint8), None, None, None, i)
     with pytest.raises(ValueError, match="device tensor"):
         rtopk.sample_filtered(torch.zeros(4, 100), torch.zeros(4))
+
+
+TREE8 = dict(q=FAKE, qs=None, kc=FAKE, vc=FAKE, cs=None, ksc=FAKE, vsc=FAKE, dtype=1, table=FAKE, ld=8, num_pages=100, page=16, lens=FAKE,
+             parents=None, sizes=None, B=2, N=4, Hq=8, Hkv=2, D=64, scale=0.125, out=FAKE, lse=None, ws=None, nws=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,status,msg", [
+    (dict(q=None), E, "NULL"), (dict(out=None), E, "NULL"), (dict(kc=None), E, "NULL"), (dict(vc=None), E, "NULL"), (dict(ksc=None), E, "NULL"),
+    (dict(vsc=None), E, "NULL"), (dict(table=None), E, "NULL"), (dict(lens=None), E, "NULL"), (dict(dtype=7), E, "dtype"),
+    (dict(dtype=0), N, "float32"), (dict(B=0), E, "sizes"), (dict(N=0), E, "sizes"), (dict(D=0), E, "sizes"), (dict(Hkv=3), E, "multiple of Hkv"),
+    (dict(D=72), N, "multiple of 16"), (dict(D=8), N, "multiple of 16"), (dict(D=272), N, "D=272"), (dict(N=257), N, "N=257"),
+    (dict(scale=math.nan), E, "scale"), (dict(scale=math.inf), E, "scale"), (dict(q=FAKE + 8), E, "q is not 16"), (dict(out=FAKE + 4), E, "out is not 16"),
+    (dict(kc=FAKE + 8), E, "k_cache is not 16"), (dict(vc=FAKE + 4), E, "v_cache is not 16"), (dict(qs=_i64(2048, 516, 64)), E, "multiple of 8"),
+    (dict(cs=_i64(2048, 136, 64)), E, "multiple of 16"), (dict(cs=_i64(2048, -128, 64)), E, "negative"), (dict(cs=_i64(2 ** 60, 128, 64)), E, "overflow"),
+    (dict(num_pages=2 ** 28), E, "2^31"), (dict(ld=2 ** 28), E, "2^31"), (dict(ld=0), E, "sizes"), (dict(page=0), E, "sizes"),
+    (dict(ws=FAKE, nws=256), rtopk.RTOPK_ENOMEM, "workspace"), (dict(ws=FAKE + 16, nws=1 << 30), E, "256-byte"), (dict(B=2 ** 20, Hq=64, Hkv=2), N, "2^31"),
+])
+def test_tree_attention_refusals(lib, kw, status, msg):
+    st, err = _call(rtopk.rtopk_tree_attention_fp8, TREE8, kw)
+    assert st == status and msg in err, err
