@@ -1,7 +1,10 @@
 // Host side of filtered sampling: argument checks and the launch. As elsewhere,
 // a rejected call touches neither the GPU nor its outputs.
 #include "rtopk.h"
+#include "rtopk_attn.h"
 #include "rtopk_filter.h"
+
+#include <exception>
 
 using rtopk::set_error;
 
@@ -36,8 +39,28 @@ extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V
     a.u = u;
     a.out_token = out_token;
     a.out_logprob = out_logprob;
-    const hipError_t e = rtopk::launch_filter(a, dtype, (hipStream_t)stream);
-    if (e != hipSuccess)
-        return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
-    return RTOPK_OK;
+    const auto go = [&](int chunks, void *ws) {
+        const hipError_t e = rtopk::launch_filter(a, dtype, chunks, ws, (hipStream_t)stream);
+        if (e != hipSuccess)
+            return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+        return (int)RTOPK_OK;
+    };
+    const int chunks = rtopk::filter_chunks(R, V);
+    if (chunks > 1) {
+        // a captured launch would keep the address of a workspace that a later call may free: it takes
+        // the form without one
+        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+        const hipError_t e = hipStreamIsCapturing((hipStream_t)stream, &cap);
+        if (e != hipSuccess)
+            return set_error(RTOPK_EHIP, "%s: hipStreamIsCapturing: %s", what, hipGetErrorString(e));
+        if (cap == hipStreamCaptureStatusNone)
+            try {
+                const size_t need = rtopk::kWsFixedBytes + R * rtopk::kFilterRowBytes;
+                return rtopk::with_workspace(need, (hipStream_t)stream,
+                                             [&](void *ws) { return go(chunks, (uint8_t *)ws + rtopk::kWsFixedBytes); });
+            } catch (const std::exception &x) { // it must not leave a C entry point
+                return set_error(RTOPK_ENOMEM, "%s: %s", what, x.what());
+            }
+    }
+    return go(1, nullptr);
 }

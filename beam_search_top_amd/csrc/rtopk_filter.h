@@ -31,6 +31,15 @@ constexpr int filter_frac(int V)
     return 62 - l < 50 ? 62 - l : 50;
 }
 
-hipError_t launch_filter(const FilterArgs &a, int dtype, hipStream_t s);
+// Workgroups per row (1: no workspace is needed).
+constexpr int kFilterChunks = 64;
+constexpr size_t kFilterRowBytes = 49920; // workspace of a row that is cut
+inline int filter_chunks(int R, int V)
+{
+    const int slots = 512 / R, most = V / 4096; // two workgroups on each of 256 CUs
+    const int c = slots < most ? slots : most;
+    return c < 2 ? 1 : c < kFilterChunks ? c : kFilterChunks;
+}
+hipError_t launch_filter(const FilterArgs &a, int dtype, int chunks, void *ws, hipStream_t s);
 
 } // namespace rtopk

@@ -22,81 +22,54 @@
 namespace rtopk {
 namespace {
 
-constexpr int kFThreads = 1024, kFWaves = kFThreads / 64;
-constexpr int kBits = 11, kBins = 1 << kBits;
+constexpr int kFThreads = 512, kFWaves = kFThreads / 64;
+constexpr int kBins = 2048;
+constexpr int kOctaves = 32;        // factors of two of weight that the bins span, at most
+constexpr int kList = 8192;          // logits that the filters may keep, of which a list is made, at most
+constexpr int kWaveList = kList / kFWaves;
+constexpr int kZone = 2 * kFThreads; // logits around the borders that are ordered one by one, at most
 
 typedef uint32_t f_u32x4 __attribute__((ext_vector_type(4)));
 
-// Logits by their order: a key is larger where the logit is; -0 is +0, a NaN is -infinity.
+// Logits as they are stored: raw bits, and how many 16 bytes hold.
 template <int DT> struct Logit;
 template <> struct Logit<0> {
     typedef uint32_t Raw;
-    static constexpr int kKeyBits = 32, kPer = 4;
-    static constexpr uint32_t kNone = 0x007fffffu; // -infinity
+    static constexpr int kPer = 4;
     static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(r); }
-    static __device__ __forceinline__ uint32_t key(uint32_t r)
-    {
-        if ((r & 0x7fffffffu) > 0x7f800000u)
-            return kNone;
-        r = r == 0x80000000u ? 0u : r;
-        return r >> 31 ? ~r : r | 0x80000000u;
-    }
-    static __device__ __forceinline__ uint32_t raw(uint32_t k) { return k >> 31 ? k & 0x7fffffffu : ~k; }
 };
-template <int DT> struct Logit16 {
+template <> struct Logit<1> {
     typedef uint16_t Raw;
-    static constexpr int kKeyBits = 16, kPer = 8;
-    static constexpr uint32_t kInf = DT == 1 ? 0x7c00u : 0x7f80u, kNone = 0xffffu ^ (kInf | 0x8000u);
-    static __device__ __forceinline__ float value(uint32_t r)
-    {
-        if constexpr (DT == 1)
-            return (float)__builtin_bit_cast(_Float16, (uint16_t)r);
-        else
-            return __uint_as_float(r << 16);
-    }
-    static __device__ __forceinline__ uint32_t key(uint32_t r)
-    {
-        if ((r & 0x7fffu) > kInf)
-            return kNone;
-        r = r == 0x8000u ? 0u : r;
-        return r >> 15 ? 0xffffu ^ r : r | 0x8000u;
-    }
-    static __device__ __forceinline__ uint32_t raw(uint32_t k) { return k >> 15 ? k & 0x7fffu : 0xffffu ^ k; }
+    static constexpr int kPer = 8;
+    static __device__ __forceinline__ float value(uint32_t r) { return (float)__builtin_bit_cast(_Float16, (uint16_t)r); }
 };
-template <> struct Logit<1> : Logit16<1> {};
-template <> struct Logit<2> : Logit16<2> {};
+template <> struct Logit<2> {
+    typedef uint16_t Raw;
+    static constexpr int kPer = 8;
+    static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(r << 16); }
+};
 
-// exp((x - top) / T) 2^frac, rounded to a whole number: 2^t by the Taylor series of
-// e^y, |y| <= ln 2 / 2, up to y^13 / 13! < 2^-52, in 64 bits.
+constexpr int kSteps = 256; // table entries per factor of two
+
+// exp((x - top) / T) 2^frac as a whole number, from t = (x - top) log2(e) / T in steps of
+// 1/256: 2^t = 2^(n / 256) 2^(r / 256), the first factor's fraction from a table, the second,
+// |r| <= 1/2, by the Taylor series up to r^4 (the next term is below 2^-54). All in 64
+// bits. Adding 2^52 rounds the result to a whole number, which the lower bits then hold.
 struct Weigh {
-    double top, by; // by = log2(e) / T
-    int frac;
+    double top, by;      // by = 256 log2(e) / T
+    const double *table; // 2^(frac + i / 256), LDS; frac <= 50
     __device__ __forceinline__ uint64_t operator()(float x) const
     {
-        const double d = (double)x - top;
-        double t = d == 0. ? 0. : d * by;
-        if ((double)x == top)
-            t = 0.; // infinities among them
-        if (!(t >= -70.) || x == -INFINITY)
-            return 0;
-        const double n = __builtin_rint(t), y = (t - n) * 0.6931471805599453;
-        double p = 1. / 479001600.;
-        p = __builtin_fma(p, y, 1. / 39916800.);
-        p = __builtin_fma(p, y, 1. / 3628800.);
-        p = __builtin_fma(p, y, 1. / 362880.);
-        p = __builtin_fma(p, y, 1. / 40320.);
-        p = __builtin_fma(p, y, 1. / 5040.);
-        p = __builtin_fma(p, y, 1. / 720.);
-        p = __builtin_fma(p, y, 1. / 120.);
-        p = __builtin_fma(p, y, 1. / 24.);
-        p = __builtin_fma(p, y, 1. / 6.);
-        p = __builtin_fma(p, y, 0.5);
-        p = __builtin_fma(p, y, 1.);
-        p = __builtin_fma(p, y, 1.);
-        const uint64_t bits = __builtin_bit_cast(uint64_t, p); // in [0.7, 1.42]
-        const int down = 52 - ((int)(bits >> 52) - 1023 + (int)n + frac); // >= 1: frac <= 50, and p < 2 at n = 0
-        const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
-        return down > 60 ? 0 : (m + (1ull << (down - 1))) >> down;
+        const double t = __builtin_fmax(((double)x - top) * by, -51200.); // -infinity, and 0 times it: 2^-200, which rounds to 0
+        const double n = __builtin_rint(t), r = t - n;
+        constexpr double c = 0.6931471805599453 / kSteps;
+        double p = __builtin_fma(c * c * c * c / 24., r, c * c * c / 6.);
+        p = __builtin_fma(p, r, c * c / 2.);
+        p = __builtin_fma(p, r, c);
+        p = __builtin_fma(p, r, 1.);
+        const int m = (int)n;
+        const double w = __builtin_ldexp(p * table[m & (kSteps - 1)], m >> 8) + 0x1p52;
+        return __builtin_bit_cast(uint64_t, w) & 0xfffffffffffffull;
     }
 };
 
@@ -117,290 +90,986 @@ template <typename T> __device__ __forceinline__ T scan_up(T x, int lane) // inc
     return x;
 }
 
-struct Bin {
-    uint32_t at;        // the bin that the border lies in
-    uint64_t above_n, n; // logits above it, in it
-    uint64_t above_w, w; // their weights
+// What a workgroup keeps in LDS.
+struct Shared {
+    double table[kSteps];
+    union {
+        uint64_t w[kBins]; // weights by bins
+        uint32_t n[kBins]; // or counts
+    };
+    uint64_t zone[kZone], sorted[kZone];
+    uint32_t list[kFWaves][kWaveList]; // tokens
+    uint64_t scan[kFWaves];
+    float2 ends[kFWaves];
+    uint32_t part32[kFWaves];
+    uint32_t count;
+    int found[2];
+    uint64_t value[4];
 };
 
-template <int DT> __global__ __launch_bounds__(kFThreads) void filter_sample(const FilterArgs a)
-{
+// Where the borders of top-k and top-p lie: bins below `sure` are kept whole, the
+// zones [p0, p1] and kb hold the borders.
+struct Borders {
+    int sure, p0, p1, kb;
+    uint32_t rest_k;  // logits of bin kb that top-k keeps
+    uint64_t above_k; // weight above bin kb
+    uint64_t above_p; // weight above bin p0
+    uint64_t all;     // of the row (or of what the list holds)
+};
+constexpr Borders kNoBorders{kBins, kBins, -1, kBins, 0, 0, 0, 0};
+
+// What keeps everything but -infinity.
+constexpr uint64_t kKeepAll = 0x00800000ull << 32;
+
+// One row and what its filters are.
+template <int DT> struct RowFilter {
     typedef Logit<DT> L;
     typedef typename L::Raw Raw;
-    constexpr int PER = L::kPer;
-    __shared__ uint64_t s_w[kBins];
-    __shared__ uint32_t s_n[kBins];
-    __shared__ uint64_t s_part[3][kFWaves];
-    __shared__ Bin s_bin;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row = blockIdx.x, V = a.V;
-    const Raw *x = static_cast<const Raw *>(a.logits) + (int64_t)row * a.ld;
-    // 16-byte pieces from the boundary at or below the row on; piece i holds elements i * PER - lead ...
-    const int lead = (int)(((uintptr_t)x & 15) / sizeof(Raw)), pieces = (int)(((int64_t)V + lead + PER - 1) / PER);
-    const f_u32x4 *base = reinterpret_cast<const f_u32x4 *>((uintptr_t)x & ~(uintptr_t)15);
-    auto element = [&](const f_u32x4 &v, int e) -> uint32_t {
+    static constexpr int PER = L::kPer;
+    const FilterArgs &a;
+    Shared &sh;
+    int row, tid, lane, wave, lead, pieces;
+    const __attribute__((address_space(1))) f_u32x4 *base;
+    float top, bin_by, bin_top; // the largest logit; bins per unit below it, and their product
+    Weigh weigh;
+    bool greedy, by_k, by_p;
+    int k;
+    float p, m;
+    uint64_t least; // min-p
+    int from, to;   // the pieces that this workgroup reads
+    int mine;       // length of this wave's list, -1: none
+    int shift;      // a run is 2^shift pieces: kBins runs hold the row
+
+    __device__ __forceinline__ RowFilter(const FilterArgs &args, Shared &shared, int r) : a(args), sh(shared), row(r)
+    {
+        tid = threadIdx.x;
+        lane = tid & 63;
+        wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const Raw *x = static_cast<const Raw *>(a.logits) + (int64_t)row * a.ld;
+        // 16-byte pieces from the boundary at or below the row on; piece i holds tokens i * PER - lead ...
+        lead = (int)(((uintptr_t)x & 15) / sizeof(Raw));
+        pieces = (int)(((int64_t)a.V + lead + PER - 1) / PER);
+        base = (const __attribute__((address_space(1))) f_u32x4 *)((uintptr_t)x & ~(uintptr_t)15);
+        from = 0;
+        to = pieces;
+        mine = -1;
+        shift = 0;
+        while ((pieces - 1) >> shift >= kBins)
+            ++shift;
+    }
+    __device__ __forceinline__ float at(int token) const // of the list
+    {
+        typedef const __attribute__((address_space(1))) Raw graw;
+        f_u32x4 v = {0, 0, 0, 0};
+        v[0] = reinterpret_cast<graw *>(base)[token + lead];
+        return value(v, 0);
+    }
+    static __device__ __forceinline__ uint32_t raw(const f_u32x4 &v, int e)
+    {
         return sizeof(Raw) == 4 ? v[e] : (e & 1 ? v[e / 2] >> 16 : v[e / 2] & 0xffffu);
-    };
-    // f(token, raw bits) for every logit of pieces i0 + lane', in steps of all threads
-    auto each = [&](auto f) {
-        for (int i = tid; i < pieces; i += kFThreads) {
-            const f_u32x4 v = base[i];
+    }
+    // A NaN is -infinity, and +infinity the largest float32, so that differences are numbers.
+    static __device__ __forceinline__ float value(const f_u32x4 &v, int e)
+    {
+        return fminf(fmaxf(L::value(raw(v, e)), -INFINITY), 0x1.fffffep127f);
+    }
+    // piece i, with -infinity in the place of what is not the row's
+    __device__ __forceinline__ f_u32x4 piece(int i) const
+    {
+        f_u32x4 v = base[i];
+        if (i == 0 || i == pieces - 1) {
+            constexpr uint32_t none = sizeof(Raw) == 4 ? 0xff800000u : DT == 1 ? 0xfc00u : 0xff80u;
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
                 const int t = i * PER + e - lead;
-                if (t >= 0 && t < V)
-                    f(t, element(v, e));
+                const bool in = t >= 0 && t < a.V;
+                if (sizeof(Raw) == 4)
+                    v[e] = in ? v[e] : none;
+                else if (e & 1)
+                    v[e / 2] = in ? v[e / 2] : (v[e / 2] & 0xffffu) | none << 16;
+                else
+                    v[e / 2] = in ? v[e / 2] : (v[e / 2] & 0xffff0000u) | none;
             }
         }
-    };
-
-    // ---- the largest
-    uint32_t best = 0;
-    each([&](int, uint32_t r) {
-        const uint32_t k = L::key(r);
-        best = k > best ? k : best;
-    });
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const uint32_t y = __shfl_xor(best, o);
-        best = y > best ? y : best;
+        return v;
     }
-    if (lane == 0)
-        s_part[0][wave] = best;
-    __syncthreads();
+    // f(token, value) for every logit of the pieces i0 + at, i0 + at + step, ... below i1, and
+    // after each piece end(piece); the next piece is on its way while one is worked on
+    template <typename F> __device__ __forceinline__ void each(int i0, int i1, int at, int step, F f) const
+    {
+        each(i0, i1, at, step, f, [](int) {});
+    }
+    template <typename F, typename G> __device__ __forceinline__ void each(int i0, int i1, int at, int step, F f, G end) const
+    {
+        int i = i0 + at;
+        if (i >= i1)
+            return;
+        f_u32x4 v = piece(i);
+        while (true) {
+            const int next = i + step;
+            f_u32x4 ahead = v;
+            if (next < i1)
+                ahead = piece(next);
 #pragma unroll
-    for (int w = 0; w < kFWaves; ++w)
-        best = s_part[0][w] > best ? (uint32_t)s_part[0][w] : best;
-    __syncthreads();
-    if (best == L::kNone) { // no candidate
-        if (tid == 0) {
-            a.out_token[row] = -1;
-            a.out_logprob[row] = -INFINITY;
+            for (int e = 0; e < PER; ++e)
+                f(i * PER + e - lead, value(v, e));
+            end(i);
+            if (next >= i1)
+                break;
+            i = next;
+            v = ahead;
         }
-        return;
     }
-    const float T = a.temperature ? a.temperature[row] : 1.f;
-    const bool greedy = !(T > 0.f);
-    const Weigh weigh{(double)L::value(L::raw(best)), greedy ? 0. : 1.4426950408889634 / (double)T, a.frac};
-    const int k = greedy ? 1 : a.top_k ? a.top_k[row] : 0;
-    float p = greedy || !a.top_p ? 1.f : a.top_p[row];
-    const bool by_k = k > 0 && k < V, by_p = p < 1.f;
-    p = p > 0.f ? p : 0.f;
-    float mp = greedy || !a.min_p ? 0.f : a.min_p[row];
-    mp = mp > 0.f ? mp < 1.f ? mp : 1.f : 0.f; // NaN: 0
-    const uint64_t least = (uint64_t)__builtin_ceil((double)mp * (double)(1ull << a.frac));
-
-    // ---- the cut
-    // Counts and weights by the next kBits bits of the keys that begin with `prefix`.
-    auto histogram = [&](uint32_t prefix, int done) {
-        for (int i = tid; i < kBins; i += kFThreads) {
-            s_w[i] = 0;
-            s_n[i] = 0;
+    // the largest and the smallest value of its pieces (-infinity apart), for every thread
+    __device__ __forceinline__ void range(float &hi, float &lo)
+    {
+        float x = -INFINITY, y = INFINITY;
+        each(from, to, tid, kFThreads, [&](int, float v) {
+            x = fmaxf(x, v);
+            y = fminf(y, v > -INFINITY ? v : INFINITY);
+        });
+        all_range(x, y);
+        hi = x;
+        lo = y;
+    }
+    __device__ __forceinline__ void all_range(float &x, float &y) // of the workgroup
+    {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            x = fmaxf(x, __shfl_xor(x, o));
+            y = fminf(y, __shfl_xor(y, o));
         }
         __syncthreads();
-        const int left = L::kKeyBits - done, take = left < kBits ? left : kBits;
-        each([&](int, uint32_t r) {
-            const uint32_t key = L::key(r);
-            if (done == 0 || key >> left == prefix) {
-                const uint32_t b = key >> (left - take) & ((1u << take) - 1);
-                atomicAdd(&s_n[b], 1u);
-                atomicAdd((unsigned long long *)&s_w[b], (unsigned long long)weigh(L::value(r)));
+        if (lane == 0)
+            sh.ends[wave] = make_float2(x, y);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kFWaves; ++w) {
+            x = fmaxf(x, sh.ends[w].x);
+            y = fminf(y, sh.ends[w].y);
+        }
+    }
+    // what is asked of the row, given its largest value and its smallest
+    __device__ __forceinline__ void ask(float hi, float lo)
+    {
+        top = hi;
+        const float T = a.temperature ? a.temperature[row] : 1.f;
+        greedy = !(T > 0.f);
+        weigh = Weigh{(double)top, greedy ? 0. : kSteps * 1.4426950408889634 / (double)T, sh.table};
+        // the bins span the row, or the logits with weights down to 2^-32 of the largest
+        const float by_weight = greedy ? 0.f : (float)((kBins / kOctaves) * 1.4426950408889634 / (double)T);
+        bin_by = fminf(fmaxf(by_weight, (float)(kBins - 1) / (hi - lo)), 0x1p126f);
+        bin_top = top * bin_by;
+        k = greedy || !a.top_k ? 0 : a.top_k[row];
+        p = greedy || !a.top_p ? 1.f : a.top_p[row];
+        by_k = k > 0 && k < a.V;
+        by_p = p < 1.f;
+        p = p > 0.f ? p : 0.f;
+        m = greedy || !a.min_p ? 0.f : a.min_p[row];
+        m = m > 0.f ? m < 1.f ? m : 1.f : 0.f; // NaN: 0
+        least = (uint64_t)__builtin_ceil((double)m * (double)(1ull << a.frac));
+        for (int i = tid; i < kSteps; i += kFThreads)
+            sh.table[i] = __builtin_ldexp(exp2((double)i / kSteps), a.frac);
+    }
+    // No logit behind this bin has the weight that min-p asks for.
+    __device__ __forceinline__ int lowest_bin() const
+    {
+        if (m == 0.f)
+            return kBins - 1;
+        const float T = a.temperature ? a.temperature[row] : 1.f;
+        const float x = -__builtin_log2f(m) * 0.6931472f * T * bin_by * (1.f + 0x1p-18f) + 2.f;
+        return x < (float)(kBins - 1) ? (int)x : kBins - 1; // (NaN: the last)
+    }
+    // A logit's bin: larger logits in lower ones. The same in every pass, since it rounds the
+    // same; far from the top, or with numbers that bin_top rounds, it is a coarse one.
+    __device__ __forceinline__ int bin(float x) const
+    {
+        return (int)__builtin_amdgcn_fmed3f(__builtin_fmaf(-x, bin_by, bin_top), 0.f, (float)(kBins - 1));
+    }
+    // The order of logits as whole numbers: larger logit first, then lower token.
+    static __device__ __forceinline__ uint64_t order(float x, int t)
+    {
+        uint32_t u = __float_as_uint(x + 0.f); // -0 is +0
+        u = u >> 31 ? ~u : u | 0x80000000u;
+        return (uint64_t)u << 32 | (uint32_t)~t;
+    }
+    static __device__ __forceinline__ float value_of(uint64_t o)
+    {
+        const uint32_t u = (uint32_t)(o >> 32);
+        return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u);
+    }
+    static __device__ __forceinline__ int token_of(uint64_t o) { return (int)~(uint32_t)o; }
+    // u times S as a whole number below S
+    __device__ __forceinline__ uint64_t point(uint64_t S) const
+    {
+        float u = a.u[row];
+        u = u > 0.f ? u : 0.f; // NaN: 0
+        const uint64_t g = u < 1.f ? (uint64_t)((double)u * (double)S) : S; // S > 0: the best is kept
+        return g < S ? g : S - 1;
+    }
+    // What top-p asks of a beginning, of a weight of `total`
+    __device__ __forceinline__ uint64_t goal_of(uint64_t total) const
+    {
+        const double want = __builtin_ceil((double)p * (double)total);
+        const uint64_t g = want < 1. ? 1 : (uint64_t)want;
+        return g < total ? g : total;
+    }
+    // The sum over the workgroup, for every thread.
+    __device__ __forceinline__ uint64_t all_sum(uint64_t x)
+    {
+        x = wave_sum(x);
+        __syncthreads();
+        if (lane == 0)
+            sh.scan[wave] = x;
+        __syncthreads();
+        x = 0;
+#pragma unroll
+        for (int i = 0; i < kFWaves; ++i)
+            x += sh.scan[i];
+        return x;
+    }
+    // The sum over the threads before this one.
+    __device__ __forceinline__ uint64_t before_me(uint64_t x)
+    {
+        const uint64_t upto = scan_up(x, lane);
+        __syncthreads();
+        if (lane == 63)
+            sh.scan[wave] = upto;
+        __syncthreads();
+        uint64_t b = upto - x;
+#pragma unroll
+        for (int i = 0; i < kFWaves; ++i)
+            b += i < wave ? sh.scan[i] : 0;
+        return b;
+    }
+
+    // ---- histograms of the pieces; the last bin is summed up apart, for it may hold most
+    __device__ __forceinline__ void clear_bins()
+    {
+        __syncthreads();
+        for (int i = tid; i < kBins; i += kFThreads)
+            sh.w[i] = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ void count_bins()
+    {
+        clear_bins();
+        uint32_t far = 0;
+        each(from, to, tid, kFThreads, [&](int, float x) {
+            const int b = bin(x);
+            if (b < kBins - 1)
+                atomicAdd(&sh.n[b], 1u);
+            else
+                ++far;
+        });
+        far = wave_sum(far);
+        if (lane == 0)
+            atomicAdd(&sh.n[kBins - 1], far);
+        __syncthreads();
+    }
+    __device__ __forceinline__ void weigh_bins()
+    {
+        clear_bins();
+        uint64_t far = 0;
+        auto add = [&](int, float x) {
+            const uint64_t w = weigh(x);
+            const int b = bin(x);
+            far += b < kBins - 1 ? 0 : w;
+            if (b < kBins - 1)
+                atomicAdd((unsigned long long *)&sh.w[b], (unsigned long long)w);
+        };
+        if (mine >= 0)
+            each_listed(add);
+        else
+            each(from, to, tid, kFThreads, add);
+        far = wave_sum(far);
+        if (lane == 0)
+            atomicAdd((unsigned long long *)&sh.w[kBins - 1], (unsigned long long)far);
+        __syncthreads();
+    }
+    // From the counts: the bin in which the first `want` logits end (found[0], kBins if there are fewer),
+    // how many of it (value[0]) they take, and the number of logits through bin `through` (value[1]).
+    __device__ __forceinline__ void find_count(uint32_t want, int through)
+    {
+        constexpr int EACH = kBins / kFThreads;
+        uint32_t n[EACH], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            n[i] = sh.n[tid * EACH + i];
+            sum += n[i];
+        }
+        uint32_t c = (uint32_t)before_me(sum);
+        if (tid == 0) {
+            sh.found[0] = kBins;
+            sh.value[0] = sh.value[1] = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int b = tid * EACH + i;
+            if (c < want && c + n[i] >= want) {
+                sh.found[0] = b;
+                sh.value[0] = want - c;
+                if (through < 0)
+                    sh.value[1] = c + n[i];
+            }
+            c += n[i];
+            if (b == through)
+                sh.value[1] = c;
+        }
+        __syncthreads();
+    }
+    // From the weights: the bin in which their running sum reaches `goal` (found[at]); value[2 at] is what
+    // lies above it.
+    __device__ __forceinline__ void find_weight(const uint64_t (&w)[kBins / kFThreads], uint64_t before, uint64_t goal, int at)
+    {
+        constexpr int EACH = kBins / kFThreads;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            if (before < goal && before + w[i] >= goal) {
+                sh.found[at] = tid * EACH + i;
+                sh.value[2 * at] = before;
+            }
+            before += w[i];
+        }
+    }
+    // The smallest value whose bin is `b` or below, or a little less.
+    __device__ __forceinline__ float floor_of(int b) const
+    {
+        if (b >= kBins - 1)
+            return -0x1.fffffep127f; // every number
+        const float x = (bin_top - (float)(b + 1)) / bin_by; // infinite or NaN where bin_by is 0
+        const float slack = (fabsf(bin_top) + (float)kBins) / bin_by * 0x1p-21f;
+        const float y = x - slack;
+        return y > -0x1.fffffep127f ? y < top ? y : top : -0x1.fffffep127f;
+    }
+    // From the counts in sh.n: where top-k's border lies. Returns the number of logits through its bin, or without
+    // top-k through bin `low`.
+    __device__ __forceinline__ uint64_t border_of_count(Borders &b, int low)
+    {
+        find_count(by_k ? (uint32_t)k : ~0u, by_k ? -1 : low);
+        if (by_k) {
+            b.kb = sh.found[0];
+            b.rest_k = (uint32_t)sh.value[0];
+        }
+        return sh.value[1];
+    }
+    // From the weights in sh.w: where top-p's border may lie. Returns about how many logits lie through it.
+    __device__ __forceinline__ float border_of_weight(Borders &b)
+    {
+        constexpr int EACH = kBins / kFThreads;
+        uint64_t w[EACH], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            w[i] = sh.w[tid * EACH + i];
+            sum += w[i];
+        }
+        const uint64_t before = before_me(sum);
+        b.all = all_sum(sum);
+        uint64_t least_left = b.all, most_left = b.all; // by top-k
+        if (by_k) {
+            uint64_t c = before;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (tid * EACH + i == b.kb) {
+                    sh.value[1] = c;
+                    sh.value[3] = w[i];
+                }
+                c += w[i];
+            }
+            __syncthreads();
+            b.above_k = sh.value[1];
+            least_left = b.above_k > 0 ? b.above_k : 1; // (something is left)
+            most_left = b.above_k + sh.value[3];
+        }
+        find_weight(w, before, goal_of(least_left), 0);
+        find_weight(w, before, goal_of(most_left), 1);
+        __syncthreads();
+        b.p0 = sh.found[0];
+        b.p1 = sh.found[1];
+        b.above_p = sh.value[0];
+        // a bin's weight over that of its middle
+        const float octave = (float)weigh.by * (1.f / kSteps) / bin_by; // of a bin
+        float n = 0.f;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int at = tid * EACH + i;
+            if (at <= b.p1)
+                n += (float)w[i] * __builtin_amdgcn_exp2f(((float)at + 0.5f) * octave - (float)a.frac);
+        }
+        return (float)all_sum((uint64_t)fminf(n, 1e9f));
+    }
+    // Sums the kept weights of its pieces (or list) by runs in sh.w, and takes the logits of the zones down in sh.zone
+    // (sh.count of them, or more than it holds).
+    __device__ __forceinline__ void weigh_kept(const Borders &b)
+    {
+        __syncthreads();
+        if (tid == 0)
+            sh.count = 0;
+        const bool zones = b.sure < kBins;
+        weigh_runs([&](int t, float x) -> uint64_t {
+            const int at = bin(x);
+            const uint64_t w = weigh(x);
+            if (zones && ((at >= b.p0 && at <= b.p1) || at == b.kb) && x > -INFINITY) {
+                const uint32_t i = atomicAdd(&sh.count, 1u);
+                if (i < kZone)
+                    sh.zone[i] = order(x, t);
+            }
+            return at < b.sure && w >= least ? w : 0;
+        });
+    }
+    // The draw, given the row's runs and zones.
+    __device__ __forceinline__ void finish(const Borders &b)
+    {
+        uint64_t cut = kKeepAll;
+        if (sh.count > kZone) {
+            cut = by_values();
+            weigh_runs([&](int t, float x) -> uint64_t {
+                const uint64_t w = order(x, t) >= cut ? weigh(x) : 0;
+                return w >= least ? w : 0;
+            });
+        } else if (by_k || by_p) {
+            const int kept = kept_of_zone(b, (int)sh.count);
+            if (kept > 0)
+                cut = sh.sorted[kept - 1];
+            for (int i = tid; i < kept; i += kFThreads) {
+                const uint64_t o = sh.sorted[i], w = weigh(value_of(o));
+                add_to_run((token_of(o) + lead) / PER, w >= least ? w : 0);
+            }
+            __syncthreads();
+        }
+        draw_from_runs(cut);
+    }
+
+    // ---- few logits that the filters may keep: the tokens of all from `floor` on go to lists, one
+    // of each wave's. False: too many.
+    __device__ __forceinline__ bool collect(float floor)
+    {
+        int n = 0;
+        uint32_t *list = sh.list[wave];
+        each(from, to, tid, kFThreads, [&](int t, float x) {
+            const uint64_t hit = __ballot(x >= floor);
+            if (hit) {
+                const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(hit >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hit, 0));
+                if (x >= floor && at < kWaveList)
+                    list[at] = (uint32_t)t;
+                n += __popcll(hit);
             }
         });
+        // lanes whose pieces end earlier have missed the last hits
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const int y = __shfl_xor(n, o);
+            n = y > n ? y : n;
+        }
         __syncthreads();
-    };
-    // The first bin from the top at which the count (or the weight) reaches `want`, given what lies above.
-    auto border = [&](bool weights, uint64_t want, uint64_t above_n, uint64_t above_w) -> Bin {
-        constexpr int EACH = kBins / kFThreads;
-        uint64_t n = 0, w = 0;
+        if (tid == 0)
+            sh.count = 0;
+        __syncthreads();
+        if (n > kWaveList)
+            sh.count = 1;
+        __syncthreads();
+        mine = sh.count ? -1 : n;
+        return mine >= 0;
+    }
+    // f(token, value) for every logit of the lists, each wave its own
+    template <typename F> __device__ __forceinline__ void each_listed(F f) const
+    {
+        for (int i = lane; i < mine; i += 64) {
+            const int t = (int)sh.list[wave][i];
+            f(t, at(t));
+        }
+    }
+    // The zone in its order, by counting: every logit's place is the number of larger ones.
+    __device__ __forceinline__ void sort_zone(int n)
+    {
+        constexpr int EACH = kZone / kFThreads;
+        uint64_t o[EACH];
+        int rank[EACH] = {};
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            o[i] = tid + i * kFThreads < n ? sh.zone[tid + i * kFThreads] : 0;
+        if (wave * 64 < n) {
+            int j = 0;
+            for (; j + 4 <= n; j += 4) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t y = sh.zone[j + q];
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i)
+                        rank[i] += y > o[i];
+                }
+            }
+            for (; j < n; ++j)
+#pragma unroll
+                for (int i = 0; i < EACH; ++i)
+                    rank[i] += sh.zone[j] > o[i];
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            if (tid + i * kFThreads < n)
+                sh.sorted[rank[i]] = o[i];
+        __syncthreads();
+    }
+    // How many of the n logits of the zones top-k and top-p keep; sh.sorted is the zone in its order.
+    __device__ __forceinline__ int kept_of_zone(const Borders &b, int n)
+    {
+        constexpr int EACH = kZone / kFThreads;
+        sort_zone(n);
+        if (!by_p)
+            return (int64_t)b.rest_k < n ? (int)b.rest_k : n;
+        uint64_t w[EACH], sum = 0;
+        uint32_t above = 0;
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            n += s_n[kBins - 1 - (tid * EACH + i)];
-            w += s_w[kBins - 1 - (tid * EACH + i)];
+            const int at = tid * EACH + i;
+            const float x = at < n ? value_of(sh.sorted[at]) : -INFINITY;
+            w[i] = at < n ? weigh(x) : 0;
+            above += at < n && bin(x) < b.kb;
+            sum += w[i];
         }
-        uint64_t cn = scan_up(n, lane), cw = scan_up(w, lane);
-        if (lane == 63) {
-            s_part[0][wave] = cn;
-            s_part[1][wave] = cw;
-        }
-        __syncthreads();
-        cn += above_n;
-        cw += above_w;
-        for (int i = 0; i < wave; ++i) {
-            cn += s_part[0][i];
-            cw += s_part[1][i];
-        }
-        cn -= n;
-        cw -= w;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int b = kBins - 1 - (tid * EACH + i);
-            const uint64_t bn = s_n[b], bw = s_w[b];
-            if (weights ? cw < want && cw + bw >= want : cn < want && cn + bn >= want)
-                s_bin = Bin{(uint32_t)b, cn, bn, cw, bw};
-            cn += bn;
-            cw += bw;
-        }
-        __syncthreads();
-        const Bin got = s_bin;
-        __syncthreads();
-        return got;
-    };
-    // The key at which the count (or the weight) reaches `want`, from the first histogram on.
-    auto search = [&](bool weights, uint64_t want, uint32_t &key) -> Bin {
-        Bin b = border(weights, want, 0, 0);
-        key = b.at;
-        for (int done = kBits; done < L::kKeyBits; done += kBits) {
-            const int take = L::kKeyBits - done < kBits ? L::kKeyBits - done : kBits;
-            histogram(key, done);
-            b = border(weights, want, b.above_n, b.above_w);
-            key = key << take | b.at;
-        }
-        return b;
-    };
-    // kept: keys above `cut`, and the first `ties` of those equal to it
-    uint32_t cut = L::kNone;
-    uint64_t ties = 0, total = 0;
-    if (by_k || by_p) {
-        histogram(0, 0);
-        if (by_p && !by_k) {
-            uint64_t w = 0;
-            for (int i = tid; i < kBins; i += kFThreads)
-                w += s_w[i];
-            w = wave_sum(w);
-            if (lane == 0)
-                s_part[2][wave] = w;
-            __syncthreads();
-            for (int i = 0; i < kFWaves; ++i)
-                total += s_part[2][i];
-        }
+        uint64_t c = before_me(sum), all = b.all;
         if (by_k) {
-            const Bin b = search(false, (uint64_t)k, cut);
-            ties = (uint64_t)k - b.above_n;
-            total = b.above_w + ties * weigh(L::value(L::raw(cut)));
+            const int k0 = (int)all_sum(above); // in front of bin kb
+            const int k1 = (int)((int64_t)k0 + b.rest_k < n ? k0 + (int)b.rest_k : n);
+            uint64_t x = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                x += tid * EACH + i >= k0 && tid * EACH + i < k1 ? w[i] : 0;
+            all = b.above_k + all_sum(x);
         }
-        if (by_p) {
-            const double want = __builtin_ceil((double)p * (double)total);
-            uint64_t goal = want < 1. ? 1 : (uint64_t)want;
-            goal = goal < total ? goal : total;
-            if (by_k)
-                histogram(0, 0);
-            const Bin b = search(true, goal, cut);
-            const uint64_t w = weigh(L::value(L::raw(cut)));
-            ties = (goal - b.above_w + w - 1) / w; // w > 0: the border lies in its bin
+        const uint64_t goal = goal_of(all) - b.above_p; // above 0: the border lies in the zone
+        uint32_t less = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            c += w[i];
+            less += tid * EACH + i < n && c < goal;
+        }
+        const int kept = (int)all_sum(less) + 1;
+        return kept < n ? kept : n;
+    }
+
+    // ---- the draw: kept weights by runs of the row, then the run that the draw falls in
+    __device__ __forceinline__ void add_to_run(int piece_index, uint64_t w)
+    {
+        if (w)
+            atomicAdd((unsigned long long *)&sh.w[piece_index >> shift], (unsigned long long)w);
+    }
+    // weight(token, value) of every logit to its run, of the list or the row
+    template <typename F> __device__ __forceinline__ void weigh_runs(F weight)
+    {
+        clear_bins();
+        if (mine >= 0) {
+            each_listed([&](int t, float x) { add_to_run((t + lead) / PER, weight(t, x)); });
+        } else {
+            uint64_t w = 0;
+            each(from, to, tid, kFThreads, [&](int t, float x) { w += weight(t, x); },
+                 [&](int i) {
+                     add_to_run(i, w);
+                     w = 0;
+                 });
+        }
+        __syncthreads();
+    }
+    // Draws, given the runs' sums, among the logits of order >= cut.
+    __device__ __forceinline__ void draw_from_runs(uint64_t cut)
+    {
+        constexpr int EACH = kBins / kFThreads;
+        uint64_t w[EACH], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            w[i] = sh.w[tid * EACH + i];
+            sum += w[i];
+        }
+        const uint64_t before = before_me(sum);
+        uint64_t S = 0; // (what the scan has left there)
+#pragma unroll
+        for (int i = 0; i < kFWaves; ++i)
+            S += sh.scan[i];
+        const uint64_t goal = point(S);
+        find_weight(w, before, goal + 1, 0);
+        __syncthreads();
+        if (wave > 0)
+            return;
+        int t = (sh.found[0] << shift) * PER - lead; // the run's first token
+        const int end = t + (PER << shift) < a.V ? t + (PER << shift) : a.V;
+        t = t > 0 ? t : 0;
+        for (uint64_t c = sh.value[0]; t < end; t += 64) {
+            uint64_t x = 0;
+            if (t + lane < end) {
+                const float y = at(t + lane);
+                x = order(y, t + lane) >= cut ? weigh(y) : 0;
+                x = x >= least ? x : 0;
+            }
+            const uint64_t upto = c + scan_up(x, lane);
+            const uint64_t hit = __ballot(upto > goal);
+            if (hit) {
+                if (lane == __ffsll((unsigned long long)hit) - 1) {
+                    a.out_token[row] = t + lane;
+                    a.out_logprob[row] = (float)log((double)x / (double)S);
+                }
+                return;
+            }
+            c = __shfl(upto, 63);
+        }
+    }
+    // The first token of its pieces that has the largest logit (~0: none), for thread 0.
+    __device__ __forceinline__ uint32_t first_of_top()
+    {
+        uint32_t first = ~0u;
+        each(from, to, tid, kFThreads, [&](int t, float x) { first = x == top && (uint32_t)t < first ? (uint32_t)t : first; });
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const uint32_t y = __shfl_xor(first, o);
+            first = y < first ? y : first;
+        }
+        __syncthreads();
+        if (lane == 0)
+            sh.part32[wave] = first;
+        __syncthreads();
+        for (int w = 0; w < kFWaves; ++w)
+            first = sh.part32[w] < first ? sh.part32[w] : first;
+        return first;
+    }
+    __device__ __forceinline__ void put(int token, float logprob)
+    {
+        if (tid == 0) {
+            a.out_token[row] = token;
+            a.out_logprob[row] = logprob;
         }
     }
 
-    // ---- the draw. A wave takes a run of consecutive pieces.
-    const uint64_t cut_w = weigh(L::value(L::raw(cut))), tie_w = cut_w >= least ? cut_w : 0;
-    const int per = (pieces + kFWaves - 1) / kFWaves, p0 = wave * per, p1 = p0 + per < pieces ? p0 + per : pieces;
-    uint64_t sum = 0, equal = 0;
-    for (int i = p0 + lane; i < p1; i += 64) {
-        const f_u32x4 v = base[i];
+    // ---- the cut of a row with many equal or nearly equal logits around a border: the border's value by
+    // its bits, 11 of them at a time, and then its tokens
+    static __device__ __forceinline__ uint32_t key(float x) { return (uint32_t)(order(x, 0) >> 32); }
+    // The value at which the count (or the weight) of the logits from the largest on reaches `want`, and what lies
+    // above it.
+    __device__ __forceinline__ float search(bool weights, uint64_t want, uint64_t &above)
+    {
+        constexpr int EACH = kBins / kFThreads;
+        uint32_t hi = key(top), lo = key(-INFINITY); // the border's key lies in [lo, hi]
+        above = 0;
+        int down = 32;
+        while (hi > lo && down > 0) { // at most three times: the range falls below 2^down
+            down = 0;
+            while ((hi - lo) >> down >= kBins)
+                ++down;
+            clear_bins();
+            each(0, pieces, tid, kFThreads, [&](int, float x) {
+                const uint32_t u = key(x);
+                if (u <= hi && u >= lo)
+                    atomicAdd((unsigned long long *)&sh.w[(hi - u) >> down], weights ? (unsigned long long)weigh(x) : 1ull);
+            });
+            __syncthreads();
+            uint64_t w[EACH], sum = 0;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int t = i * PER + e - lead;
-            if (t >= 0 && t < V) {
-                const uint32_t r = element(v, e), key = L::key(r);
-                if (key > cut) {
-                    const uint64_t w = weigh(L::value(r));
-                    sum += w >= least ? w : 0;
-                }
-                equal += key == cut;
+            for (int i = 0; i < EACH; ++i) {
+                w[i] = sh.w[tid * EACH + i];
+                sum += w[i];
+            }
+            find_weight(w, above + before_me(sum), want, 0);
+            __syncthreads();
+            above = sh.value[0];
+            hi -= (uint32_t)sh.found[0] << down;
+            const uint32_t least_key = hi - ((1u << down) - 1);
+            lo = least_key > lo && least_key <= hi ? least_key : lo;
+        }
+        return value_of((uint64_t)hi << 32);
+    }
+    // The order of the last logit that top-k and top-p leave.
+    __device__ __forceinline__ uint64_t by_values()
+    {
+        float v = 0.f;
+        uint64_t ties = 0, above;
+        if (by_k) {
+            v = search(false, (uint64_t)k, above);
+            ties = (uint64_t)k - above;
+        }
+        if (by_p) {
+            uint64_t w = 0; // of what top-k leaves
+            each(0, pieces, tid, kFThreads, [&](int, float x) { w += !by_k || x > v ? weigh(x) : 0; });
+            const uint64_t goal = goal_of(all_sum(w) + (by_k ? ties * weigh(v) : 0));
+            v = search(true, goal, above);
+            const uint64_t one = weigh(v);
+            ties = (goal - above + one - 1) / one; // above 0: the border lies there
+        }
+        // the token of the last tie that is kept
+        const int per = (pieces + kFWaves - 1) / kFWaves, p0 = wave * per, p1 = p0 + per < pieces ? p0 + per : pieces;
+        uint32_t n = 0;
+        each(p0, p1, lane, 64, [&](int, float x) { n += x == v; });
+        n = wave_sum(n);
+        __syncthreads();
+        if (lane == 0)
+            sh.scan[wave] = n;
+        __syncthreads();
+        uint64_t before = 0;
+        for (int i = 0; i < wave; ++i)
+            before += sh.scan[i];
+        if (before < ties && ties <= before + n) {
+            for (int j = p0; j < p1; j += 64) {
+                const int i = j + lane;
+                f_u32x4 q = {0, 0, 0, 0};
+                if (i < p1)
+                    q = piece(i);
+                uint32_t own = 0;
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    own += i < p1 && value(q, e) == v;
+                const uint32_t upto = scan_up(own, lane);
+                uint64_t at = before + upto - own; // ties in front
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    if (i < p1 && value(q, e) == v && ++at == ties)
+                        sh.value[3] = order(v, i * PER + e - lead);
+                before += __shfl(upto, 63);
             }
         }
+        __syncthreads();
+        return sh.value[3];
     }
-    sum = wave_sum(sum);
-    equal = wave_sum(equal);
-    if (lane == 0) {
-        s_part[0][wave] = sum;
-        s_part[1][wave] = equal;
-    }
-    __syncthreads();
-    uint64_t S = 0, before = 0, ties_before = 0, seen = 0;
-    uint64_t start[kFWaves];
-#pragma unroll
-    for (int i = 0; i < kFWaves; ++i) {
-        start[i] = S;
-        if (i == wave)
-            ties_before = seen;
-        const uint64_t room = ties > seen ? ties - seen : 0, mine = s_part[1][i] < room ? s_part[1][i] : room;
-        S += s_part[0][i] + mine * tie_w;
-        seen += s_part[1][i];
-    }
-    float u = a.u[row];
-    u = u > 0.f ? u : 0.f; // NaN: 0
-    uint64_t goal = u < 1.f ? (uint64_t)((double)u * (double)S) : S; // S > 0: the best is kept
-    goal = goal < S ? goal : S - 1;
-    // the run that the running sum passes the goal in
-    bool mine = false;
-#pragma unroll
-    for (int i = 0; i < kFWaves; ++i)
-        if (i == wave) {
-            before = start[i];
-            mine = start[i] <= goal && (i + 1 < kFWaves ? start[i + 1 < kFWaves ? i + 1 : i] : S) > goal;
-        }
-    if (!mine)
+};
+
+// A workgroup per row. Every pass but the first reads the row from L2.
+//   1. The largest logit.
+//   2. Where the filters' borders lie, to 1/64 of a factor of two of weight: logits are counted (top-k, min-p) or
+//      weighed (top-p) by bins that are linear in the logit.
+//   3. Where few logits lie above the borders, as usual, a list is made of them, and what follows reads
+//      it instead of the row.
+//   4. The logits of the bins in which the borders lie are ordered one by one, which gives the cut. A row
+//      with too many equal or nearly equal ones finds it by the bits of the logits.
+//   5. Kept weights are summed by runs of the row, and the run that the draw falls in is read again.
+template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(const FilterArgs a)
+{
+    __shared__ Shared sh;
+    RowFilter<DT> f(a, sh, blockIdx.x);
+    float hi, lo;
+    f.range(hi, lo);
+    if (hi == -INFINITY) {
+        f.put(-1, -INFINITY);
         return;
-    for (int i0 = p0; i0 < p1; i0 += 64) {
-        const int i = i0 + lane;
-        f_u32x4 v = {0, 0, 0, 0};
-        if (i < p1)
-            v = base[i];
-        uint64_t w[PER], n = 0;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int t = i * PER + e - lead;
-            const bool in = i < p1 && t >= 0 && t < V;
-            n += in && L::key(element(v, e)) == cut;
-        }
-        const uint64_t upto = scan_up(n, lane);
-        uint64_t rank = ties_before + upto - n, own = 0;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int t = i * PER + e - lead;
-            const bool in = i < p1 && t >= 0 && t < V;
-            const uint32_t r = element(v, e), key = L::key(r);
-            w[e] = 0;
-            if (in && key > cut) {
-                w[e] = weigh(L::value(r));
-                w[e] = w[e] >= least ? w[e] : 0;
-            } else if (in && key == cut) {
-                w[e] = rank < ties ? tie_w : 0;
-                ++rank;
-            }
-            own += w[e];
-        }
-        const uint64_t sums = scan_up(own, lane);
-        const uint64_t hit = __ballot(before + sums > goal);
-        if (hit) {
-            if (lane == __ffsll((unsigned long long)hit) - 1) {
-                uint64_t c = before + sums - own;
-                int e = 0;
-                while (e < PER - 1 && c + w[e] <= goal)
-                    c += w[e++];
-                a.out_token[row] = i * PER + e - lead;
-                a.out_logprob[row] = (float)log((double)w[e] / (double)S);
-            }
-            return;
-        }
-        before += __shfl(sums, 63);
-        ties_before += __shfl(upto, 63);
     }
+    f.ask(hi, lo);
+    if (f.greedy) {
+        f.put((int)f.first_of_top(), 0.f);
+        return;
+    }
+    __syncthreads(); // the table
+    Borders b = kNoBorders;
+    const int low = f.lowest_bin();
+    for (int stage = 0; stage < 2; ++stage) {
+        int last = kBins; // the last bin of the list, if it can hold all
+        if (stage == 0) {
+            if (!f.by_k && (f.m == 0.f || f.by_p))
+                continue;
+            f.count_bins();
+            if (f.border_of_count(b, low) <= kList)
+                last = f.by_k ? b.kb : low;
+        } else {
+            if (!f.by_p)
+                continue;
+            f.weigh_bins();
+            if (f.border_of_weight(b) <= kList && !f.by_k)
+                last = low < b.p1 ? low : b.p1;
+        }
+        if (last < kBins && f.mine < 0)
+            f.collect(f.floor_of(last));
+    }
+    b.sure = f.by_p ? b.p0 : f.by_k ? b.kb : kBins;
+    f.weigh_kept(b);
+    f.finish(b);
+}
+
+// ---- few rows: each cut into `chunks` of whole runs, a workgroup each, in three launches that pass
+// histograms, sums and zones through the workspace.
+struct alignas(256) SplitRow {
+    uint64_t w[kBins], runs[kBins], zone[kZone];
+    uint32_t n[kBins];
+    float2 ends[kFilterChunks];
+    uint32_t count, ticket, first;
+};
+static_assert(sizeof(SplitRow) == kFilterRowBytes, "rtopk_filter.h");
+
+// What one workgroup writes and another reads within a launch goes through the device's coherence point.
+__device__ __forceinline__ void put64(uint64_t *p, uint64_t x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint64_t get64(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+template <int DT> __device__ __forceinline__ void take_chunk(RowFilter<DT> &f, int chunk, int chunks)
+{
+    const int runs = ((f.pieces - 1) >> f.shift) + 1, per = (runs + chunks - 1) / chunks;
+    f.from = (chunk * per) << f.shift;
+    f.from = f.from < f.pieces ? f.from : f.pieces;
+    f.to = ((chunk + 1) * per) << f.shift;
+    f.to = f.to < f.pieces ? f.to : f.pieces;
+}
+
+template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_range(const FilterArgs a, SplitRow *rows, int chunks)
+{
+    __shared__ Shared sh;
+    const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+    RowFilter<DT> f(a, sh, row);
+    take_chunk(f, chunk, chunks);
+    SplitRow &s = rows[row];
+    for (int i = chunk * kFThreads + f.tid; i < kBins; i += chunks * kFThreads) {
+        s.w[i] = 0;
+        s.n[i] = 0;
+    }
+    if (chunk == 0 && f.tid == 0) {
+        s.count = s.ticket = 0;
+        s.first = ~0u;
+    }
+    float hi, lo;
+    f.range(hi, lo);
+    if (f.tid == 0)
+        s.ends[chunk] = make_float2(hi, lo);
+}
+
+// The ends of the row from those of its chunks.
+template <int DT> __device__ __forceinline__ void row_range(RowFilter<DT> &f, const SplitRow &s, int chunks, float &hi, float &lo)
+{
+    hi = -INFINITY;
+    lo = INFINITY;
+    if (f.tid < chunks) {
+        hi = s.ends[f.tid].x;
+        lo = s.ends[f.tid].y;
+    }
+    f.all_range(hi, lo);
+}
+
+template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_bins(const FilterArgs a, SplitRow *rows, int chunks)
+{
+    __shared__ Shared sh;
+    const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+    RowFilter<DT> f(a, sh, row);
+    take_chunk(f, chunk, chunks);
+    SplitRow &s = rows[row];
+    float hi, lo;
+    row_range(f, s, chunks, hi, lo);
+    if (hi == -INFINITY)
+        return;
+    f.ask(hi, lo);
+    if (f.by_k) {
+        f.count_bins();
+        for (int i = f.tid; i < kBins; i += kFThreads)
+            if (sh.n[i])
+                atomicAdd(&s.n[i], sh.n[i]);
+    }
+    if (f.by_p) {
+        __syncthreads(); // the table
+        f.weigh_bins();
+        for (int i = f.tid; i < kBins; i += kFThreads)
+            if (sh.w[i])
+                atomicAdd((unsigned long long *)&s.w[i], (unsigned long long)sh.w[i]);
+    }
+}
+
+template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(const FilterArgs a, SplitRow *rows, int chunks)
+{
+    __shared__ Shared sh;
+    const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+    RowFilter<DT> f(a, sh, row);
+    take_chunk(f, chunk, chunks);
+    SplitRow &s = rows[row];
+    float hi, lo;
+    row_range(f, s, chunks, hi, lo);
+    if (hi == -INFINITY) {
+        if (chunk == 0)
+            f.put(-1, -INFINITY);
+        return;
+    }
+    f.ask(hi, lo);
+    Borders b = kNoBorders;
+    if (f.greedy) {
+        const uint32_t first = f.first_of_top();
+        if (f.tid == 0 && first != ~0u)
+            atomicMin(&s.first, first);
+    } else {
+        __syncthreads(); // the table
+        if (f.by_k) {
+            f.clear_bins();
+            for (int i = f.tid; i < kBins; i += kFThreads)
+                sh.n[i] = s.n[i];
+            __syncthreads();
+            f.border_of_count(b, 0);
+        }
+        if (f.by_p) {
+            __syncthreads();
+            for (int i = f.tid; i < kBins; i += kFThreads)
+                sh.w[i] = s.w[i];
+            __syncthreads();
+            f.border_of_weight(b);
+        }
+        b.sure = f.by_p ? b.p0 : f.by_k ? b.kb : kBins;
+        f.weigh_kept(b);
+        // its runs and its part of the zones
+        const int r0 = f.from >> f.shift, r1 = (f.to + (1 << f.shift) - 1) >> f.shift;
+        for (int i = r0 + f.tid; i < r1; i += kFThreads)
+            put64(&s.runs[i], sh.w[i]);
+        const uint32_t n = sh.count;
+        if (n > 0) {
+            if (f.tid == 0)
+                sh.found[0] = (int)__hip_atomic_fetch_add(&s.count, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            const uint32_t at = (uint32_t)sh.found[0];
+            for (uint32_t i = f.tid; i < n && i < kZone; i += kFThreads)
+                if (at + i < kZone)
+                    put64(&s.zone[at + i], sh.zone[i]);
+        }
+    }
+    // the last workgroup of the row to arrive draws
+    __builtin_amdgcn_s_waitcnt(0x0f70); // this wave's stores are done
+    __syncthreads();
+    if (f.tid == 0)
+        sh.found[1] = __hip_atomic_fetch_add(&s.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)chunks - 1;
+    __syncthreads();
+    if (!sh.found[1])
+        return;
+    if (f.greedy) {
+        f.put((int)__hip_atomic_load(&s.first, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), 0.f);
+        return;
+    }
+    const int runs = ((f.pieces - 1) >> f.shift) + 1;
+    for (int i = f.tid; i < kBins; i += kFThreads)
+        sh.w[i] = i < runs ? get64(&s.runs[i]) : 0;
+    const uint32_t n = __hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (uint32_t i = f.tid; i < n && i < kZone; i += kFThreads)
+        sh.zone[i] = get64(&s.zone[i]);
+    if (f.tid == 0)
+        sh.count = n;
+    f.from = 0;
+    f.to = f.pieces;
+    __syncthreads();
+    f.finish(b);
+}
+
+template <int DT> hipError_t launch_type(const FilterArgs &a, int chunks, void *ws, hipStream_t s)
+{
+    const dim3 block(kFThreads);
+    if (chunks == 1) {
+        hipLaunchKernelGGL(filter_row<DT>, dim3((unsigned)a.R), block, 0, s, a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(a.R * chunks));
+    SplitRow *rows = static_cast<SplitRow *>(ws);
+    hipLaunchKernelGGL(filter_range<DT>, grid, block, 0, s, a, rows, chunks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    if (a.top_k || a.top_p) {
+        hipLaunchKernelGGL(filter_bins<DT>, grid, block, 0, s, a, rows, chunks);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL(filter_draw<DT>, grid, block, 0, s, a, rows, chunks);
+    return hipGetLastError();
 }
 
 } // namespace
 
-hipError_t launch_filter(const FilterArgs &a, int dtype, hipStream_t s)
+hipError_t launch_filter(const FilterArgs &a, int dtype, int chunks, void *ws, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.R), block(kFThreads);
-    if (dtype == 0)
-        hipLaunchKernelGGL(filter_sample<0>, grid, block, 0, s, a);
-    else if (dtype == 1)
-        hipLaunchKernelGGL(filter_sample<1>, grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL(filter_sample<2>, grid, block, 0, s, a);
-    return hipGetLastError();
+    return dtype == 0   ? launch_type<0>(a, chunks, ws, s)
+           : dtype == 1 ? launch_type<1>(a, chunks, ws, s)
+                        : launch_type<2>(a, chunks, ws, s);
 }
 
 } // namespace rtopk

@@ -590,9 +590,11 @@ int rtopk_tree_attention_fp8(const void *q, const int64_t *q_strides, const void
  *   out_token  device [R] int32; out_logprob device [R] float32
  * Weights are computed in 64 bits and summed as whole numbers of 2^-f, f = min(50,
  * 62 - ceil(log2 V)), so that sums are exact and the same call gives the same result;
- * a candidate of weight below 2^-(f+1) is never drawn. Logits as in rtopk_beam_step
- * otherwise. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`;
- * one launch, no workspace.
+ * a candidate of weight below 2^-(f+1) is never drawn. The largest float32 counts as
+ * infinite. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`. Few
+ * long rows are cut over workgroups, which takes three launches and the library-owned
+ * workspace that rtopk_cross_attention describes (calls on one stream come from one thread
+ * at a time); under graph capture a call takes one launch and none, with the same results.
  */
 int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
