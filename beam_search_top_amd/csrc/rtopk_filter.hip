@@ -30,6 +30,8 @@ constexpr int kWaveList = kList / kFWaves;
 constexpr int kZone = 2 * kFThreads; // logits around the borders that are ordered one by one, at most
 
 typedef uint32_t f_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+constexpr int kSortStep = 16; // logits of the zone that are on their way together
 
 // Logits as they are stored: raw bits, and how many 16 bytes hold.
 template <int DT> struct Logit;
@@ -97,7 +99,8 @@ struct Shared {
         uint64_t w[kBins]; // weights by bins
         uint32_t n[kBins]; // or counts
     };
-    uint64_t zone[kZone], sorted[kZone];
+    alignas(16) uint64_t zone[kZone];
+    uint64_t sorted[kZone];
     uint32_t list[kFWaves][kWaveList]; // tokens
     uint64_t scan[kFWaves];
     float2 ends[kFWaves];
@@ -121,8 +124,10 @@ constexpr Borders kNoBorders{kBins, kBins, -1, kBins, 0, 0, 0, 0};
 // What keeps everything but -infinity.
 constexpr uint64_t kKeepAll = 0x00800000ull << 32;
 
-// One row and what its filters are.
-template <int DT> struct RowFilter {
+// One row and what its filters are. SHORT: the loop over the logits of 16 bytes is not unrolled. A
+// launch of few rows meets its code for the first time everywhere (about 80 ns for each 64 bytes of
+// it), which costs more than the loop (8 x 250000: 31 us of the last launch's with unrolled loops, XX without).
+template <int DT, bool SHORT> struct RowFilter {
     typedef Logit<DT> L;
     typedef typename L::Raw Raw;
     static constexpr int PER = L::kPer;
@@ -210,9 +215,19 @@ template <int DT> struct RowFilter {
             f_u32x4 ahead = v;
             if (next < i1)
                 ahead = piece(next);
+            if constexpr (SHORT) {
+#pragma unroll 1
+                for (int e = 0; e < PER; e += PER / 4) {
+                    f(i * PER + e - lead, value(v, 0));
+                    if constexpr (PER == 8)
+                        f(i * PER + e + 1 - lead, value(v, 1));
+                    v = __builtin_shufflevector(v, v, 1, 2, 3, 0);
+                }
+            } else {
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-                f(i * PER + e - lead, value(v, e));
+                for (int e = 0; e < PER; ++e)
+                    f(i * PER + e - lead, value(v, e));
+            }
             end(i);
             if (next >= i1)
                 break;
@@ -343,6 +358,16 @@ template <int DT> struct RowFilter {
         return b;
     }
 
+    // The sum over the workgroup of what before_me has just scanned.
+    __device__ __forceinline__ uint64_t scanned() const
+    {
+        uint64_t x = 0;
+#pragma unroll
+        for (int i = 0; i < kFWaves; ++i)
+            x += sh.scan[i];
+        return x;
+    }
+
     // ---- histograms of the pieces; the last bin is summed up apart, for it may hold most
     __device__ __forceinline__ void clear_bins()
     {
@@ -454,8 +479,8 @@ template <int DT> struct RowFilter {
         }
         return sh.value[1];
     }
-    // From the weights in sh.w: where top-p's border may lie. Returns about how many logits lie through it.
-    __device__ __forceinline__ float border_of_weight(Borders &b)
+    // From the weights in sh.w: where top-p's border may lie.
+    __device__ __forceinline__ void border_of_weight(Borders &b)
     {
         constexpr int EACH = kBins / kFThreads;
         uint64_t w[EACH], sum = 0;
@@ -465,7 +490,7 @@ template <int DT> struct RowFilter {
             sum += w[i];
         }
         const uint64_t before = before_me(sum);
-        b.all = all_sum(sum);
+        b.all = scanned();
         uint64_t least_left = b.all, most_left = b.all; // by top-k
         if (by_k) {
             uint64_t c = before;
@@ -488,14 +513,17 @@ template <int DT> struct RowFilter {
         b.p0 = sh.found[0];
         b.p1 = sh.found[1];
         b.above_p = sh.value[0];
-        // a bin's weight over that of its middle
-        const float octave = (float)weigh.by * (1.f / kSteps) / bin_by; // of a bin
+    }
+    // From the weights in sh.w: about how many logits lie through bin `last`.
+    __device__ __forceinline__ float number_through(int last)
+    {
+        const float octaves = (float)weigh.by * (1.f / kSteps) / bin_by; // of a bin
         float n = 0.f;
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int at = tid * EACH + i;
-            if (at <= b.p1)
-                n += (float)w[i] * __builtin_amdgcn_exp2f(((float)at + 0.5f) * octave - (float)a.frac);
+        for (int i = 0; i < kBins / kFThreads; ++i) {
+            const int at = i * kFThreads + tid;
+            if (at <= last) // its weight over that of its middle
+                n += (float)sh.w[at] * __builtin_amdgcn_exp2f(((float)at + 0.5f) * octaves - (float)a.frac);
         }
         return (float)all_sum((uint64_t)fminf(n, 1e9f));
     }
@@ -580,35 +608,43 @@ template <int DT> struct RowFilter {
             f(t, at(t));
         }
     }
-    // The zone in its order, by counting: every logit's place is the number of larger ones.
-    __device__ __forceinline__ void sort_zone(int n)
+    // The zone in its order, by counting: every logit's place is the number of larger ones (455 of them: 5 us;
+    // 2 us at 100).
+    template <int EACH> __device__ __forceinline__ void place_zone(int n)
     {
-        constexpr int EACH = kZone / kFThreads;
         uint64_t o[EACH];
         int rank[EACH] = {};
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
             o[i] = tid + i * kFThreads < n ? sh.zone[tid + i * kFThreads] : 0;
-        if (wave * 64 < n) {
-            int j = 0;
-            for (; j + 4 <= n; j += 4) {
+        const u64x2 *from = reinterpret_cast<const u64x2 *>(sh.zone);
+        for (int j = 0; j < n; j += kSortStep) {
+            u64x2 y[kSortStep / 2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint64_t y = sh.zone[j + q];
+            for (int q = 0; q < kSortStep / 2; ++q)
+                y[q] = from[j / 2 + q];
 #pragma unroll
-                    for (int i = 0; i < EACH; ++i)
-                        rank[i] += y > o[i];
-                }
-            }
-            for (; j < n; ++j)
+            for (int q = 0; q < kSortStep / 2; ++q)
 #pragma unroll
                 for (int i = 0; i < EACH; ++i)
-                    rank[i] += sh.zone[j] > o[i];
+                    rank[i] += (int)(y[q][0] > o[i]) + (int)(y[q][1] > o[i]);
         }
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
             if (tid + i * kFThreads < n)
                 sh.sorted[rank[i]] = o[i];
+    }
+    __device__ __forceinline__ void sort_zone(int n)
+    {
+        // (padded with zeros to whole steps, which are below every logit)
+        if (tid < kSortStep && n + tid < kZone)
+            sh.zone[n + tid] = 0;
+        __syncthreads();
+        static_assert(kZone == 2 * kFThreads, "two logits per thread");
+        if (n > kFThreads)
+            place_zone<2>(n);
+        else if (wave * 64 < n)
+            place_zone<1>(n);
         __syncthreads();
     }
     // How many of the n logits of the zones top-k and top-p keep; sh.sorted is the zone in its order.
@@ -682,10 +718,7 @@ template <int DT> struct RowFilter {
             sum += w[i];
         }
         const uint64_t before = before_me(sum);
-        uint64_t S = 0; // (what the scan has left there)
-#pragma unroll
-        for (int i = 0; i < kFWaves; ++i)
-            S += sh.scan[i];
+        const uint64_t S = scanned();
         const uint64_t goal = point(S);
         find_weight(w, before, goal + 1, 0);
         __syncthreads();
@@ -841,7 +874,7 @@ template <int DT> struct RowFilter {
 template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(const FilterArgs a)
 {
     __shared__ Shared sh;
-    RowFilter<DT> f(a, sh, blockIdx.x);
+    RowFilter<DT, false> f(a, sh, blockIdx.x);
     float hi, lo;
     f.range(hi, lo);
     if (hi == -INFINITY) {
@@ -868,7 +901,8 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(con
             if (!f.by_p)
                 continue;
             f.weigh_bins();
-            if (f.border_of_weight(b) <= kList && !f.by_k)
+            f.border_of_weight(b);
+            if (!f.by_k && f.number_through(b.p1) <= kList)
                 last = low < b.p1 ? low : b.p1;
         }
         if (last < kBins && f.mine < 0)
@@ -893,7 +927,7 @@ static_assert(sizeof(SplitRow) == kFilterRowBytes, "rtopk_filter.h");
 __device__ __forceinline__ void put64(uint64_t *p, uint64_t x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t get64(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-template <int DT> __device__ __forceinline__ void take_chunk(RowFilter<DT> &f, int chunk, int chunks)
+template <int DT> __device__ __forceinline__ void take_chunk(RowFilter<DT, true> &f, int chunk, int chunks)
 {
     const int runs = ((f.pieces - 1) >> f.shift) + 1, per = (runs + chunks - 1) / chunks;
     f.from = (chunk * per) << f.shift;
@@ -906,7 +940,7 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_range(c
 {
     __shared__ Shared sh;
     const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-    RowFilter<DT> f(a, sh, row);
+    RowFilter<DT, true> f(a, sh, row);
     take_chunk(f, chunk, chunks);
     SplitRow &s = rows[row];
     for (int i = chunk * kFThreads + f.tid; i < kBins; i += chunks * kFThreads) {
@@ -924,7 +958,7 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_range(c
 }
 
 // The ends of the row from those of its chunks.
-template <int DT> __device__ __forceinline__ void row_range(RowFilter<DT> &f, const SplitRow &s, int chunks, float &hi, float &lo)
+template <int DT> __device__ __forceinline__ void row_range(RowFilter<DT, true> &f, const SplitRow &s, int chunks, float &hi, float &lo)
 {
     hi = -INFINITY;
     lo = INFINITY;
@@ -939,7 +973,7 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_bins(co
 {
     __shared__ Shared sh;
     const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-    RowFilter<DT> f(a, sh, row);
+    RowFilter<DT, true> f(a, sh, row);
     take_chunk(f, chunk, chunks);
     SplitRow &s = rows[row];
     float hi, lo;
@@ -966,7 +1000,7 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
 {
     __shared__ Shared sh;
     const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-    RowFilter<DT> f(a, sh, row);
+    RowFilter<DT, true> f(a, sh, row);
     take_chunk(f, chunk, chunks);
     SplitRow &s = rows[row];
     float hi, lo;
@@ -1030,11 +1064,10 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
     const int runs = ((f.pieces - 1) >> f.shift) + 1;
     for (int i = f.tid; i < kBins; i += kFThreads)
         sh.w[i] = i < runs ? get64(&s.runs[i]) : 0;
-    const uint32_t n = __hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (uint32_t i = f.tid; i < n && i < kZone; i += kFThreads)
+    for (int i = f.tid; i < kZone; i += kFThreads) // (what lies behind the zone's logits is not used)
         sh.zone[i] = get64(&s.zone[i]);
     if (f.tid == 0)
-        sh.count = n;
+        sh.count = __hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     f.from = 0;
     f.to = f.pieces;
     __syncthreads();
