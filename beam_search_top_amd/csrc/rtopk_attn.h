@@ -84,7 +84,7 @@ struct AttnPlan {
     size_t ml_off, part_off, ws_bytes; // workspace behind the fixed region
 };
 // wide: rows of keys or values lie 2^25 elements or more apart (not for attn_few)
-AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide);
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide, bool fp8);
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, int dtype, bool tree, hipStream_t s);
 hipError_t launch_attention_fp8(const AttnArgs8 &a, const AttnPlan &p, int dtype, hipStream_t s); // a tree
 

@@ -89,6 +89,13 @@ template <int CH> __device__ __forceinline__ constexpr int fv(int r)
     return CH == 8 ? (r & 2) << 1 | (r >> 1 & 2) : (r & 3) << 2 | (r >> 1 & 2);
 }
 
+// The same for the keys of attn_few, whose chunks are 16 bytes: of codes 16 elements. 16 rows at
+// one chunk fall on different banks.
+template <int CH> __device__ __forceinline__ constexpr int ff(int r)
+{
+    return !kF8 ? fk<CH>(r) : CH == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+
 // What attn_tiles loads in the place of a key that does not count.
 __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
@@ -925,7 +932,13 @@ __device__ __forceinline__ uint64_t get64(const void *p)
 }
 
 constexpr int kFewWaves = 4;
-constexpr int kFewStep = 32; // keys per step of a wave
+// Workgroups per CU that the registers of attn_few have to leave room for. 8 bits, one row: with heads of 64 three
+// (2 requests of 90000 and 131000 keys of 16 heads: 134 us, with four, which spill, 153); with heads of 128 two (8
+// heads: 98 us, three, which spill, 103).
+constexpr int few_waves(int dp, int nb) { return kF8 && nb == 1 && dp == 64 ? 3 : 2; }
+// Keys per step of a wave. 64 of 64 codes: half as many bytes on their way were too few (2 x 440000 keys of 16
+// heads: 414 us, with 32 500 us; with 128 codes 64 make no difference, and two blocks of rows spill).
+constexpr int few_step(int dp) { return kF8 && dp == 64 ? 64 : 32; }
 
 // A workgroup's share: steps [begin, end) of batch element b, one of `parts`
 // shares of it; `unit` numbers the shares of all batch elements, `unit0` is
@@ -938,7 +951,7 @@ struct Share {
 // them at most: long and short batch elements load the GPU evenly, which the host
 // cannot do without knowing the lengths. Every wave sums the lengths by itself
 // (B <= 256). A batch element with rows has at least one share.
-template <bool TREE> __device__ __forceinline__ Share find_share(const AttnArgs &a, int unit, int lane)
+template <bool TREE, int kFewStep> __device__ __forceinline__ Share find_share(const AttnArgs &a, int unit, int lane)
 {
     Share s{-1, 0, 0, 0, unit, 0};
     int tiles[4], total = 0, longest = 0;
@@ -997,17 +1010,20 @@ template <bool TREE> __device__ __forceinline__ Share find_share(const AttnArgs 
     return s;
 }
 
-// MODE 0: cross attention; 1: a tree, pages of a multiple of 8 tokens; 2: a tree, other pages.
-// (Modes of one kernel, not branches in it: the counts by which a wave waits for
+// MODE 0: cross attention; 1: a tree, pages of a multiple of the rows of one load (8; of 64 codes 16) in
+// tokens; 2: a tree, other pages. (Modes of one kernel, not branches in it: the counts by which a wave waits for
 // its older loads only must be the same on every path.)
 template <int DT, int DP, int NB, int MODE>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
+__global__ __launch_bounds__(64 * kFewWaves, few_waves(DP, NB)) void attn_few(const Args a)
 {
     constexpr bool TREE = MODE != 0;
+    constexpr int kFewStep = few_step(DP), GROUPS = kFewStep / 32; // keys of a step, products with the values over them
+    typedef std::conditional_t<kFewStep == 64, uint64_t, uint32_t> Mask;
     typedef Elem<DT> E;
     typedef typename E::T T;
     constexpr int VE = DP / 16, DC = DP / 32, VW = VE / 2; // columns per lane, products per score, value dwords
-    constexpr int ROWB = DP * 2, CH = DP / 8, RPL = 1024 / ROWB, NK = kFewStep / RPL; // a 1 KiB load is RPL rows
+    constexpr int ROWB = DP * kElemBytes, CH = ROWB / 16, RPL = 1024 / ROWB, NK = kFewStep / RPL; // a 1 KiB load is RPL rows
+    constexpr int VL = kF8 ? VE / 4 : VW; // value dwords as they are loaded
     constexpr int PITCH = DP + 4;
     constexpr int KEYS = kFewWaves * kFewStep * ROWB, OUTS = kFewWaves * 16 * PITCH * 4;
     // the waves' keys; after the loop their outputs, a block of 16 rows at a time
@@ -1023,7 +1039,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     const int xi = (int)blockIdx.x / 8, hk = xi % a.Hkv, unit = xi / a.Hkv * 8 + (int)blockIdx.x % 8;
     Share sh;
     if (a.units > 0) {
-        sh = find_share<TREE>(a, unit, lane);
+        sh = find_share<TREE, kFewStep>(a, unit, lane);
         if (sh.b < 0)
             return;
     } else {
@@ -1044,8 +1060,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     const int t_begin = sh.begin, t_end = a.units > 0 ? sh.end : (kr.end + kFewStep - 1) / kFewStep, parts = sh.parts;
 
     // ---- loads
-    gchar *kbase = (gchar *)a.k + 2 * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
-    gchar *vbase = (gchar *)a.v + 2 * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
+    gchar *kbase = (gchar *)a.k + kElemBytes * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
+    gchar *vbase = (gchar *)a.v + kElemBytes * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
     uint8_t *mine = smem + wave * kFewStep * ROWB;
     // Step t is rows first(t) ... + 31. Past the last row that can be read (cross: S
     // >= 32) it begins earlier and leaves out the keys of the step before.
@@ -1057,7 +1073,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     };
     // what decides about key first(t) + lane mod 32, read ahead: its page, or its mask
     auto fetch = [&](int t) -> int {
-        const int j = first(t) + (lane & 31);
+        const int j = first(t) + (lane & (kFewStep - 1));
         if (t >= t_end || j >= kr.end)
             return -1;
         if (TREE)
@@ -1068,22 +1084,24 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     // be read (tree: the cache's first rows); their scores are replaced and their
     // values zeroed where they are used.
     struct Step {
-        uint32_t oks; // the keys that count
+        Mask oks;     // the keys that count
         int64_t off;  // tree: byte offset of this lane's key
+        int slot;     // 8 bits: its slot
     };
     auto place = [&](int t, int info) -> Step {
-        const int j = first(t) + (lane & 31);
+        const int j = first(t) + (lane & (kFewStep - 1));
         bool ok = t < t_end && j >= t * kFewStep && j < kr.end;
-        Step s{0, 0};
+        Step s{0, 0, 0};
         if (TREE) {
             const int id = checked_page(info, a.num_pages);
             ok = ok && id >= 0;
             const int pg = (int)page_of(a.page, (uint32_t)(ok ? j : 0));
-            s.off = ok ? 2 * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : 0;
+            s.off = ok ? kElemBytes * (id * a.ks[0] + (int64_t)(j - pg * (int)a.page.d) * a.ks[1]) : 0;
+            s.slot = ok ? id * (int)a.page.d + (j - pg * (int)a.page.d) : 0;
         } else {
             ok = ok && info == 0;
         }
-        s.oks = (uint32_t)__ballot(ok);
+        s.oks = (Mask)__ballot(ok);
         return s;
     };
     // Row u + lane_r of a step (u the same for the wave) lies at a base of the wave's and a
@@ -1091,8 +1109,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     // host sees to it that 32 of them span less than 2^32 bytes), up to 8 rows of a tree lie on
     // one page where pages allow it. Else every lane has a 64-bit offset of its own.
     const int lrow = lane / CH, lchunk = lane % CH;
-    const uint32_t kstep = 2 * (uint32_t)a.ks[1], vstep = 2 * (uint32_t)a.vs[1];
-    const uint32_t kcol = lchunk * 8 < a.D ? lchunk * 16 : 0, vcol = VE * col < a.D ? 2 * VE * col : 0;
+    constexpr int CE = 16 / kElemBytes; // elements of a chunk
+    const uint32_t kstep = kElemBytes * (uint32_t)a.ks[1], vstep = kElemBytes * (uint32_t)a.vs[1];
+    const uint32_t kcol = lchunk * CE < a.D ? lchunk * 16 : 0, vcol = VE * col < a.D ? kElemBytes * VE * col : 0;
     const uint32_t klane = lrow * kstep + kcol, vlane = grp * vstep + vcol;
     auto row = [&](gchar *base, const Step &s, int t, int u, int lane_r, uint32_t step, uint32_t lane_off, uint32_t lane_col) -> gchar * {
         // behind the last step, every lane reads the same line
@@ -1105,21 +1124,39 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
             return base + (int64_t)((uint64_t)(uint32_t)__shfl((int)(s.off >> 32), u + lane_r) << 32 |
                                     (uint32_t)__shfl((int)s.off, u + lane_r)) + (t < t_end ? lane_col : 0);
     };
+    // 64-byte rows are half lines: the next head's workgroup reads the other half soon after (and fetches the line
+    // again if the first load has marked it as read once: 137 against 115 us)
+    auto fetch_row = [](auto *p) {
+        if constexpr (ROWB < 128)
+            return *p;
+        else
+            return __builtin_nontemporal_load(p);
+    };
     u32x4 kq[NK];
     auto load_keys = [&](const Step &s, int t) {
 #pragma unroll
         for (int i = 0; i < NK; ++i)
-            kq[i] = __builtin_nontemporal_load((gu32x4 *)row(kbase, s, t, i * RPL, lrow, kstep, klane, kcol));
+            kq[i] = fetch_row((gu32x4 *)row(kbase, s, t, i * RPL, lrow, kstep, klane, kcol));
     };
-    uint32_t vq[8][VW];
+    // 8 bits: the scales of key and value `lane` of the step
+    auto load_scale = [&](const Step &s) -> uint32_t {
+        if constexpr (kF8) {
+            const int64_t at = (int64_t)s.slot * a.Hkv + hk;
+            return k_scales(a)[at] | (uint32_t)v_scales(a)[at] << 16;
+        }
+        return 0;
+    };
+    uint32_t vq[8 * GROUPS][VL];
     auto load_values = [&](const Step &s, int t) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8 * GROUPS; ++j) {
             gchar *p = row(vbase, s, t, 4 * j, grp, vstep, vlane, vcol);
-            if constexpr (VW == 4) {
+            if constexpr (VL == 1) {
+                vq[j][0] = fetch_row((const __attribute__((address_space(1))) uint32_t *)p);
+            } else if constexpr (VL == 4) {
                 const u32x4 y = __builtin_nontemporal_load((gu32x4 *)p);
 #pragma unroll
-                for (int x = 0; x < VW; ++x)
+                for (int x = 0; x < VL; ++x)
                     vq[j][x] = y[x];
             } else {
                 const u32x2 y = __builtin_nontemporal_load((gu32x2 *)p);
@@ -1150,6 +1187,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     int t = t_begin + wave;
     Step now = place(t, fetch(t));
     load_keys(now, t);
+    uint32_t scale = load_scale(now);
     int info = fetch(t + kFewWaves);
     load_values(now, t);
 
@@ -1197,33 +1235,46 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
     }
     for (; t < t_end; t += kFewWaves) {
         const bool in_tree = walk && (t + 1) * kFewStep > kr.tree0;
-        const bool masked = now.oks != ~0u || in_tree;
+        const bool masked = now.oks != (Mask)~(Mask)0 || in_tree;
         // ---- scores
         if (a.D < DP) { // elements past the head's are zeros in both operands
 #pragma unroll
             for (int i = 0; i < NK; ++i)
-                kq[i] = lchunk * 8 < a.D ? kq[i] : u32x4{0, 0, 0, 0};
+                kq[i] = lchunk * CE < a.D ? kq[i] : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int r = i * RPL + lrow;
-            *reinterpret_cast<u32x4 *>(mine + r * ROWB + (lchunk ^ fk<CH>(r)) * 16) = kq[i];
+            *reinterpret_cast<u32x4 *>(mine + r * ROWB + (lchunk ^ ff<CH>(r)) * 16) = kq[i];
         }
+        // of key and value `lane`
+        const uint32_t kby = kF8 ? scale_bits(held_scale(scale & 0xffu)) : 0, vby = kF8 ? scale_bits(held_scale(scale >> 16)) : 0;
         const Step next = place(t + kFewWaves, info);
         load_keys(next, t + kFewWaves);
+        scale = load_scale(next);
         info = fetch(t + 2 * kFewWaves);
         // this wave's own LDS, which serves it in order: no other wave to wait for
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        f32x4 x[NB][2];
+        f32x4 x[NB][2 * GROUPS];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2 * GROUPS; ++k) {
             const int r = 16 * k + kr0;
             u32x4 kf[DC];
+            if constexpr (kF8) {
+                const float f = __uint_as_float((uint32_t)__shfl((int)kby, r));
 #pragma unroll
-            for (int c = 0; c < DC; ++c)
-                kf[c] = *reinterpret_cast<const u32x4 *>(mine + r * ROWB + ((4 * c + grp) ^ fk<CH>(r)) * 16);
+                for (int c = 0; c < DC; ++c) {
+                    const u32x2 y = *reinterpret_cast<const u32x2 *>(mine + r * ROWB + ((2 * c + grp / 2) ^ ff<CH>(r)) * 16 + grp % 2 * 8);
+                    kf[c] = u32x4{E::template decoded<false>(y[0], f), E::template decoded<true>(y[0], f),
+                                  E::template decoded<false>(y[1], f), E::template decoded<true>(y[1], f)};
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < DC; ++c)
+                    kf[c] = *reinterpret_cast<const u32x4 *>(mine + r * ROWB + ((4 * c + grp) ^ ff<CH>(r)) * 16);
+            }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 x[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1233,31 +1284,31 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
             }
         }
         // ---- weights
-        uint32_t see[NB];
-        u32x4 p[NB];
+        Mask see[NB];
+        u32x4 p[NB][GROUPS];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             see[n] = now.oks;
             if (in_tree) {
-                const int off = t * kFewStep - kr.tree0; // node of the step's first key: above -32
-                see[n] &= off < 0 ? (up[n] << -off) | ((1u << -off) - 1) : off < 32 ? up[n] >> off : 0;
+                const int off = t * kFewStep - kr.tree0; // node of the step's first key: above -kFewStep
+                see[n] &= off < 0 ? ((Mask)up[n] << -off) | (((Mask)1 << -off) - 1) : off < 32 ? up[n] >> off : 0;
             }
-            const uint32_t bits = see[n] >> grp;
+            const Mask bits = see[n] >> grp;
             if (masked || far[n]) {
                 if (far[n]) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < 2 * GROUPS; ++k)
                         x[n][k] *= cs;
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2 * GROUPS; ++k)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         x[n][k][i] = bits >> (16 * k + 4 * i) & 1 ? x[n][k][i] : -INFINITY;
             }
             float mx = x[n][0][0];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2 * GROUPS; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     mx = fmaxf(mx, x[n][k][i]);
@@ -1270,7 +1321,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
                     far[n] = true;
                     ce[n] = 1.f;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < 2 * GROUPS; ++k)
                         x[n][k] *= cs;
                 }
                 l[n] *= f;
@@ -1279,49 +1330,98 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
                     o[n][y] *= f;
             }
             const float mu = m[n] == -INFINITY ? 0.f : m[n];
-            T y[8];
+            T y[GROUPS][8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2 * GROUPS; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k][i], ce[n], -mu));
                     if (masked && cs == 0.f) // 0 * -inf is not -inf
                         e = bits >> (16 * k + 4 * i) & 1 ? e : 0.f;
                     l[n] += e;
-                    y[4 * k + i] = (T)e;
+                    y[k / 2][4 * (k % 2) + i] = (T)e;
                 }
-            p[n] = __builtin_bit_cast(u32x4, y);
-        }
-        if (now.oks != ~0u) { // 0 * infinity: a value that does not count must be finite
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < VW; ++e)
-                    vq[j][e] = now.oks >> (4 * j + grp) & 1 ? vq[j][e] : 0u;
+            for (int g = 0; g < GROUPS; ++g)
+                p[n][g] = __builtin_bit_cast(u32x4, y[g]);
         }
-        // ---- a node's infinities and NaN, as in attn_tiles
         bool odd = false;
-        if (TREE && in_tree) {
+        if constexpr (kF8) {
+            // two columns at a time as numbers of the type of q; what is done about places that do not count and about
+            // a node's NaN is as below
+            if (now.oks != (Mask)~(Mask)0) { // (code 0 is 0)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 8 * GROUPS; ++j)
 #pragma unroll
-                for (int e = 0; e < VW; ++e) {
-                    const bool lo = (vq[j][e] & E::kExp) == E::kExp, hi = (vq[j][e] >> 16 & E::kExp) == E::kExp;
-                    odd = odd || lo || hi;
-                    vq[j][e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                    for (int e = 0; e < VL; ++e)
+                        vq[j][e] = now.oks >> (4 * j + grp) & 1 ? vq[j][e] : 0u;
+                asm volatile("" ::: "memory"); // a branch, not a selection in every step
+            }
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                float vf[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    vf[j] = __uint_as_float((uint32_t)__shfl((int)vby, 32 * g + 4 * j + grp));
+#pragma unroll
+                for (int y = 0; y < VE; y += 2) {
+                    uint32_t d[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        d[j] = y % 4 ? E::template decoded<true>(vq[8 * g + j][y / 4], vf[j])
+                                     : E::template decoded<false>(vq[8 * g + j][y / 4], vf[j]);
+                    if (in_tree) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const bool lo = (d[j] & E::kExp) == E::kExp, hi = (d[j] >> 16 & E::kExp) == E::kExp;
+                            odd = odd || lo || hi;
+                            d[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        u32x4 v;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], h ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            o[n][y + h] = Small<DT>::mfma(v, p[n][g], o[n][y + h]);
+                    }
                 }
-            odd = __any(odd);
-        }
-        // ---- outputs
+            }
+            odd = in_tree && __any(odd);
+        } else {
+            if (now.oks != ~0u) { // 0 * infinity: a value that does not count must be finite
 #pragma unroll
-        for (int y = 0; y < VE; ++y) {
-            u32x4 v;
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = __builtin_amdgcn_perm(vq[2 * j + 1][y / 2], vq[2 * j][y / 2], y % 2 ? 0x07060302u : 0x05040100u);
+                    for (int e = 0; e < VW; ++e)
+                        vq[j][e] = now.oks >> (4 * j + grp) & 1 ? vq[j][e] : 0u;
+            }
+            // ---- a node's infinities and NaN, as in attn_tiles
+            if (TREE && in_tree) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-                o[n][y] = Small<DT>::mfma(v, p[n], o[n][y]);
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        const bool lo = (vq[j][e] & E::kExp) == E::kExp, hi = (vq[j][e] >> 16 & E::kExp) == E::kExp;
+                        odd = odd || lo || hi;
+                        vq[j][e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                    }
+                odd = __any(odd);
+            }
+            // ---- outputs
+#pragma unroll
+            for (int y = 0; y < VE; ++y) {
+                u32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = __builtin_amdgcn_perm(vq[2 * j + 1][y / 2], vq[2 * j][y / 2], y % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    o[n][y] = Small<DT>::mfma(v, p[n][0], o[n][y]);
+            }
         }
         load_values(next, t + kFewWaves);
         if (TREE && odd) {
@@ -1330,7 +1430,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
                     continue;
                 const int pos = t * kFewStep + j, pg = (int)page_of(a.page, (uint32_t)pos);
                 const int id = a.table[(int64_t)b * a.ld + pg]; // a page of the cache: the key counts
-                const T *vr = static_cast<const T *>(a.v) + hk * a.vs[2] + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+                typedef std::conditional_t<kF8, uint8_t, T> C;
+                const C *vr = static_cast<const C *>(a.v) + hk * a.vs[2] + id * a.ks[0] + (int64_t)(pos - pg * (int)a.page.d) * a.ks[1];
+                uint8_t its = 0; // scale
+                if constexpr (kF8)
+                    its = v_scales(a)[((int64_t)id * (int)a.page.d + (pos - pg * (int)a.page.d)) * a.Hkv + hk];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1338,6 +1442,16 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few(const Args a)
                         const int e = VE * (4 * grp + i) + y;
                         if (e >= a.D)
                             continue;
+                        if constexpr (kF8) {
+                            const T x = element8<E>(vr[e], its);
+                            if ((__builtin_bit_cast(uint16_t, x) & E::kExp) != E::kExp)
+                                continue;
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                if (see[n] >> j & 1)
+                                    o[n][y][i] += (float)x;
+                            continue;
+                        }
                         const uint16_t raw = reinterpret_cast<const uint16_t *>(vr)[e];
                         if ((raw & E::kExp) != E::kExp)
                             continue;
@@ -1531,11 +1645,11 @@ template <int DT, int DP, bool TREE> __global__ __launch_bounds__(256) void attn
 template <int DT, int DP, bool TREE> hipError_t launch_dims(const Args &a, const AttnPlan &p, hipStream_t s)
 {
     const dim3 grid((unsigned)p.grid);
-    if constexpr (DP <= 128 && !kF8) {
+    if constexpr (DP <= 128) {
         if (p.few) {
             const dim3 block(64 * kFewWaves);
             if constexpr (TREE) {
-                const bool even = a.page.d % 8 == 0;
+                const bool even = a.page.d % (kF8 && DP == 64 ? 16 : 8) == 0;
                 if (p.few == 1 && even)
                     hipLaunchKernelGGL((attn_few<DT, DP, 1, 1>), grid, block, 0, s, a);
                 else if (p.few == 1)

@@ -36,9 +36,15 @@ constexpr int kFilterChunks = 64;
 constexpr size_t kFilterRowBytes = 49920; // workspace of a row that is cut
 inline int filter_chunks(int R, int V)
 {
-    const int slots = 512 / R, most = V / 4096; // two workgroups on each of 256 CUs
-    const int c = slots < most ? slots : most;
-    return c < 2 ? 1 : c < kFilterChunks ? c : kFilterChunks;
+    // Three launches and the workspace between them cost about 17 us whatever the size; a row's own workgroup takes
+    // 20 to 40 us per 40000 logits, and leaves CUs idle up to 256 rows. us cut / not: 1 x 16000 18 / 12, 16 x 24000
+    // 30 / 27, 64 x 24000 35 / 29; 1 x 32000 19 / 21, 32 x 32000 27 / 40, 128 x 32000 39 / 41, 128 x 100000 64 / 89,
+    // 8 x 250000 37 / 200; 200 x 40000 55 / 43, 256 x 100000 100 / 90.
+    const int most = V / 4096;
+    if (R > 128 || most < 7)
+        return 1;
+    const int slots = 512 / R, c = slots < most ? slots : most; // two workgroups on each of 256 CUs
+    return c < kFilterChunks ? c : kFilterChunks;
 }
 hipError_t launch_filter(const FilterArgs &a, int dtype, int chunks, void *ws, hipStream_t s);
 

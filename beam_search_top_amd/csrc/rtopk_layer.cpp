@@ -132,10 +132,10 @@ bool cache8_wide(const rtopk::Cache8Args &a)
 }
 
 // Workspace of a call whatever its strides.
-size_t attention_bytes(int B, int N, int Hq, int Hkv, int D, int S)
+size_t attention_bytes(int B, int N, int Hq, int Hkv, int D, int S, bool fp8 = false)
 {
-    const size_t x = rtopk::plan_attention(B, N, Hq, Hkv, D, S, false).ws_bytes;
-    const size_t y = rtopk::plan_attention(B, N, Hq, Hkv, D, S, true).ws_bytes;
+    const size_t x = rtopk::plan_attention(B, N, Hq, Hkv, D, S, false, fp8).ws_bytes;
+    const size_t y = rtopk::plan_attention(B, N, Hq, Hkv, D, S, true, fp8).ws_bytes;
     return x > y ? x : y;
 }
 
@@ -143,8 +143,8 @@ int enqueue_attention(const char *what, rtopk::AttnArgs8 &a, int dtype, bool tre
                       hipStream_t stream)
 {
     // attn_few holds the offsets of 32 rows in 32 bits, and needs 32 rows to read
-    const bool wide = fp8 || a.ks[1] >= (1 << 25) || a.vs[1] >= (1 << 25) || (!tree && a.S < 32);
-    const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S, wide);
+    const bool wide = a.ks[1] >= (1 << 25) || a.vs[1] >= (1 << 25) || (!tree && a.S < 32);
+    const rtopk::AttnPlan p = rtopk::plan_attention(a.B, a.N, a.Hq, a.Hkv, a.D, a.S, wide, fp8);
     if (workspace && (uintptr_t)workspace % 256)
         return set_error(RTOPK_EINVAL, "%s: workspace is not 256-byte aligned", what);
     if (workspace && ws_bytes < p.ws_bytes)
@@ -234,7 +234,7 @@ int tree_attention(const char *what, bool fp8, const void *q, const int64_t *q_s
 
 namespace rtopk {
 
-AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
+AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide, bool fp8)
 {
     AttnPlan p{};
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
@@ -253,7 +253,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide)
         // with 3 and 8 the call above takes 107 and 110 us). 128 x 16 of them are not
         // cut: 34 us, cut in two or more 44 us, for the ends of every share cost more
         // than the balance gains.
-        p.bn = 32;
+        p.bn = fp8 && p.dp == 64 ? 64 : 32; // few_step
         p.waves = 4;
         p.row_tiles = 1;
         p.min_tiles = 4;
@@ -565,6 +565,14 @@ size_t rtopk_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D
         table_ld < 1 || page < 1 || !mul_fits(table_ld, page, INT_MAX - 4096))
         return 0;
     return attention_bytes(B, N, Hq, Hkv, D, table_ld * page);
+}
+
+size_t rtopk_tree_attention_fp8_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int table_ld, int page)
+{
+    if (check_attention("8-bit tree attention", RTOPK_F16, B, N, Hq, Hkv, D, 1.f) != RTOPK_OK || N > rtopk::kMaxTree ||
+        D % 16 || table_ld < 1 || page < 1 || !mul_fits(table_ld, page, INT_MAX - 4096))
+        return 0;
+    return attention_bytes(B, N, Hq, Hkv, D, table_ld * page, true);
 }
 
 size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hkv, int D)

@@ -115,6 +115,8 @@ def load():
     L.rtopk_tree_attention_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, i32, i32, i32,
                                            i32, i32, ctypes.c_float, vp, vp, vp, sz, vp]
     L.rtopk_tree_attention_fp8.restype = i32
+    L.rtopk_tree_attention_fp8_workspace_bytes.argtypes = [i32] * 7
+    L.rtopk_tree_attention_fp8_workspace_bytes.restype = sz
     L.rtopk_sample_filtered.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp]
     L.rtopk_sample_filtered.restype = i32
     L.rtopk_read_probe.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
@@ -355,6 +357,10 @@ def rtopk_tree_attention_fp8(q, q_strides, k_cache, v_cache, cache_strides, k_sc
     return load().rtopk_tree_attention_fp8(q, q_strides, k_cache, v_cache, cache_strides, k_scales, v_scales, dtype, table,
                                            table_ld, num_pages, page, cache_lens, parents, sizes, B, N, Hq, Hkv, D, scale,
                                            out, lse, workspace, ws_bytes, stream)
+
+
+def rtopk_tree_attention_fp8_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page):
+    return load().rtopk_tree_attention_fp8_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page)
 
 
 def rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token, out_logprob, stream):
@@ -878,7 +884,8 @@ def tree_attention_fp8(q, k_cache, v_cache, k_scales, v_scales, table, cache_len
                        out=None, lse=None, workspace=None):
     """tree_attention over a cache in 8 bits, as cache_store_fp8 fills it: k_cache, v_cache
     [pages, page, Hkv, D] float8_e4m3fn (or uint8), D a multiple of 16, and k_scales, v_scales
-    [pages, page, Hkv] uint8; everything else as tree_attention. Returns (out, lse)."""
+    [pages, page, Hkv] uint8; everything else as tree_attention (a workspace has
+    rtopk_tree_attention_fp8_workspace_bytes(...) bytes). Returns (out, lse)."""
     _get_torch()
     if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")

@@ -559,14 +559,14 @@ int rtopk_cache_load_fp8(const void *k_cache, const void *v_cache, const int64_t
  * tensors of that type; an element beyond the type's range becomes infinite, and one
  * with bits below its smallest number is rounded). D is a multiple of 16; k_cache,
  * v_cache 16-byte aligned, cache_strides in bytes and multiples of 16. Everything
- * else as rtopk_tree_attention; the workspace is that of
- * rtopk_tree_attention_workspace_bytes.
+ * else as rtopk_tree_attention; its workspace's size is a function of its own.
  */
 int rtopk_tree_attention_fp8(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
                              const int64_t *cache_strides, const uint8_t *k_scales, const uint8_t *v_scales, int dtype,
                              const int32_t *table, int table_ld, int num_pages, int page, const int32_t *cache_lens,
                              const int32_t *parents, const int32_t *sizes, int B, int N, int Hq, int Hkv, int D, float scale,
                              void *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
+size_t rtopk_tree_attention_fp8_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int table_ld, int page);
 
 /*
  * Sampling with temperature, top-k, top-p and min-p from given random numbers.

@@ -267,7 +267,7 @@ def test_graph_replays(N):
     pages, page, Hkv, _ = c["kc"].shape
     g = _gen(N)
     ld = c["table"].shape[1]
-    ws = torch.zeros(rtopk.rtopk_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, ld, page), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(rtopk.rtopk_tree_attention_fp8_workspace_bytes(B, N, Hq, Hkv, D, ld, page), dtype=torch.uint8, device=DEV)
     x = torch.randn(B, N, Hq + 2 * Hkv, D, generator=g, device=DEV).to(F16)
     freqs = (10000.0 ** (-torch.arange(0, D, 2, device=DEV) / D)).float()
     pos = c["lens"][:, None] + torch.arange(N, device=DEV, dtype=torch.int32)
@@ -312,7 +312,7 @@ def test_capture_without_a_workspace_is_refused():
     c = _inputs(1, 1, 2, 2, 64, 16, [20000], F16, seed=1)  # few rows, many keys: split
     want = _call(c)[0].clone()
     out = torch.zeros_like(want)
-    ws = torch.zeros(rtopk.rtopk_tree_attention_workspace_bytes(1, 1, 2, 2, 64, c["table"].shape[1], 16), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(rtopk.rtopk_tree_attention_fp8_workspace_bytes(1, 1, 2, 2, 64, c["table"].shape[1], 16), dtype=torch.uint8, device=DEV)
     graph = torch.cuda.CUDAGraph()
     err = None
     with torch.cuda.graph(graph):
