@@ -126,7 +126,7 @@ constexpr uint64_t kKeepAll = 0x00800000ull << 32;
 
 // One row and what its filters are. SHORT: the loop over the logits of 16 bytes is not unrolled. A
 // launch of few rows meets its code for the first time everywhere (about 80 ns for each 64 bytes of
-// it), which costs more than the loop (8 x 250000: 31 us of the last launch's with unrolled loops, XX without).
+// it), which costs more than the loop (the last launch of 8 x 250000: 31 us with unrolled loops, 26 without).
 template <int DT, bool SHORT> struct RowFilter {
     typedef Logit<DT> L;
     typedef typename L::Raw Raw;
@@ -1034,8 +1034,8 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
         }
         b.sure = f.by_p ? b.p0 : f.by_k ? b.kb : kBins;
         f.weigh_kept(b);
-        // its runs and its part of the zones
-        const int r0 = f.from >> f.shift, r1 = (f.to + (1 << f.shift) - 1) >> f.shift;
+        // its runs and its part of the zones (a chunk behind the row's end has no run: the row's last may end early)
+        const int r0 = f.from >> f.shift, r1 = f.from < f.to ? (f.to + (1 << f.shift) - 1) >> f.shift : r0;
         for (int i = r0 + f.tid; i < r1; i += kFThreads)
             put64(&s.runs[i], sh.w[i]);
         const uint32_t n = sh.count;

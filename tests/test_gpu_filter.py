@@ -187,3 +187,98 @@ def test_agrees_with_the_top_k_step():
     for r in range(64):
         at = (lists[1][r] == tok[r]).nonzero()
         assert at.numel() == 1 and abs(float(p[r, at[0, 0]]) - float(lp[r])) < 1e-4
+
+
+def _both_forms(x, u, what, oracle=True, **f):
+    """Few long rows are cut over workgroups, but not in a captured call: both give the same."""
+    R = x.shape[0]
+    d = lambda a, dt: None if a is None else torch.tensor([a] * R if np.isscalar(a) else a, dtype=dt, device=DEV)  # noqa: E731
+    ud = torch.tensor(np.asarray(u, dtype=np.float32), device=DEV)
+    kw = dict(temperature=d(f.get("t"), F32), top_k=d(f.get("k"), torch.int32), top_p=d(f.get("p"), F32), min_p=d(f.get("m"), F32))
+    out = (torch.zeros(R, dtype=torch.int32, device=DEV), torch.zeros(R, device=DEV))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rtopk.sample_filtered(x, ud, out=out, **kw)
+    eager = rtopk.sample_filtered(x, ud, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    one, other = [[t.tolist() for t in pair] for pair in (out, eager)]
+    assert one == other, what
+    return _check(x, u, what, **f) if oracle else tuple(other)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("R,V,ld,shift", [(1, 28672, 28672, 0), (1, 28671, 28671, 0), (3, 40001, 40003, 3), (2, 100003, 100004, 1), (2, 250000, 250000, 0),
+                                          (1, 270007, 270007, 7)])
+def test_rows_cut_over_workgroups(R, V, ld, shift, dt):
+    print(f"[filter cut] R={R} V={V} ld={ld} {dt}", flush=True)
+    y, rng = _rows(1, (R - 1) * ld + V + shift, dt, seed=V + R, sigma=2.0)
+    x = torch.as_strided(y, (R, V), (ld, 1), shift)
+    for what, kw in dict(none={}, t=dict(t=0.8), k=dict(k=64), m=dict(m=0.01), p=dict(p=0.95), wide=dict(p=0.999), all=dict(t=0.9, k=900, p=0.9, m=0.001),
+                         many=dict(k=V - 5, p=0.9999), greedy=dict(t=0.0)).items():
+        _both_forms(x, rng.random(R), what, **kw)
+    # equal logits: a draw lands on token floor(u V), in the first and the last run of the row too
+    flat = torch.as_strided(torch.zeros_like(y), (R, V), (ld, 1), shift)
+    for n in (0, 1, V // 2, V - 40, V - 9, V - 2, V - 1):
+        tok, _ = _both_forms(flat, [(n + 0.5) / V] * R, f"flat {n}", oracle=False)
+        assert tok == [n] * R  # u is rounded by 2^-25 at most, V 2^-25 of a token
+
+
+@pytest.mark.parametrize("R,V", [(128, 28672), (129, 28672), (64, 33000), (300, 1000)])
+def test_numbers_of_rows(R, V):
+    x, rng = _rows(R, V, BF16, seed=R)
+    u = rng.random(R)
+    for kw in (dict(p=0.9), dict(k=50, p=0.95, m=0.02, t=0.9), dict()):
+        tok, lp = _both_forms(x, u, str(kw), oracle=False, **kw)
+        some = [0, 1, R // 2, R - 1]
+        assert _check(x[some].contiguous(), u[some], str(kw), **kw) == ([tok[r] for r in some], [lp[r] for r in some])
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("V", [9000, 40000])
+def test_many_equal_and_many_kept(V, dt):
+    # borders among more equal logits, and kept sets of more, than a workgroup holds
+    rng = np.random.default_rng(V)
+    levels = torch.tensor([0.0, 0.5, 1.0, 1.5], device=DEV)
+    at = torch.tensor(rng.integers(0, 4, (6, V)), device=DEV)
+    x = levels[at].to(dt)
+    u = rng.random(6)
+    n = int((at[0] == 3).sum())
+    for kw in (dict(k=n - 1), dict(k=n), dict(k=n + 1), dict(k=V - 7), dict(p=0.3), dict(p=0.77), dict(k=2 * n, p=0.8), dict(k=n // 2, p=0.5, m=0.3),
+               dict(m=0.5), dict(p=1e-6), dict(p=0.999999)):
+        _both_forms(x, u, str(kw), **kw)
+    near = (torch.tensor(rng.random((6, V)), device=DEV) * 0.01).to(dt)
+    for kw in (dict(p=0.9), dict(k=V // 2), dict(k=V // 2, p=0.9), dict(m=0.995), dict(p=0.9, m=0.995)):
+        _both_forms(near, u, "near " + str(kw), **kw)
+    x[:, 1:] = float("-inf")
+    for kw in (dict(p=0.5), dict(k=3), dict(k=3, p=0.1, m=0.2)):
+        tok, lp = _both_forms(x, u, "one " + str(kw), **kw)
+        assert tok == [0] * 6 and lp == [0.0] * 6
+
+
+def test_long_rows_on_two_streams():
+    x, rng = _rows(4, 150000, F16, seed=21)
+    y, _ = _rows(6, 90000, F16, seed=22)
+    u = torch.tensor(rng.random(6), dtype=F32, device=DEV)
+    p = torch.full((6,), 0.97, device=DEV)
+    call = lambda z: rtopk.sample_filtered(z, u[:z.shape[0]], top_p=p[:z.shape[0]])  # noqa: E731
+    want = call(x), call(y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = []
+        for s, z in zip(streams, (x, y)):
+            with torch.cuda.stream(s):
+                got.append([call(z) for _ in range(5)])
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for one in g for a, b in zip(one, w))
+
+
+def test_odd_temperatures():
+    x, rng = _rows(6, 31000, F32, seed=23, sigma=2.0)
+    u = rng.random(6)
+    inf = float("inf")
+    _both_forms(x, u, "t", t=[inf, 1e-40, 1e38, 2.0 ** -126, 3e-39, 0.3])
+    _both_forms(x, u, "t p", t=[1e-40, 1e-20, 1e38, 5.0, 1e-3, 0.3], p=0.9)
+    _both_forms(x, u, "t k", t=[inf, 1e-20, 1e38, 5.0, 1e-3, 0.3], k=700)
