@@ -2,7 +2,7 @@
 (serve_ref.sample): the same tokens, and their log-probabilities.
 
 A token may differ where a running sum comes within the sums' error of a border: the
-kernel's weights are off by 2^-44 of the largest at V = 250000 (2^-50 below 4096), a
+kernel's weights are off by 2^-44 of the largest at V = 250000 (2^-48 below 4096), a
 sum of n of them by 2^-44 sqrt(n), which is under 2^-35 of the sum; with a border every
 2^-18 of it that is one row in 2^17 for flat rows and far fewer for others. The inputs are
 fixed. Log-probabilities are rounded once, and log(w / S) is off by at most 2^-24 in absolute terms for
