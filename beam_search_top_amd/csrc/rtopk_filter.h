@@ -7,7 +7,7 @@
 namespace rtopk {
 
 constexpr int kFilterMaxV = 1 << 24; // 38 bits behind a weight's binary point
-constexpr int kFilterMaxR = 1 << 20; // a workgroup of 1024 threads each: a launch counts its threads in 32 bits
+constexpr int kFilterMaxR = 1 << 20; // a workgroup of 512 threads each: a launch counts its threads in 32 bits
 
 struct FilterArgs {
     const void *logits;  // [R][ld]

@@ -533,8 +533,9 @@ int rtopk_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, c
  *              [3] (page, token, head) in bytes, the same for both
  *   k_scales, v_scales  device [num_pages][page][Hkv] uint8, contiguous
  *   dtype      type of k and v, any of the three; D <= 256 (else RTOPK_ENOTSUP)
- * Everything else as rtopk_cache_store. Rows move 16 elements at a time when D is
- * a multiple of 16 and pointers and strides of 16 bytes, else one by one.
+ * Everything else as rtopk_cache_store; where two tokens name one slot, its codes and
+ * its scales may come from different ones of them. Rows move 16 elements at a time when
+ * D is a multiple of 16 and pointers and strides of 16 bytes, else one by one.
  */
 int rtopk_cache_store_fp8(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides, int dtype,
                           const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache,

@@ -282,3 +282,32 @@ def test_odd_temperatures():
     _both_forms(x, u, "t", t=[inf, 1e-40, 1e38, 2.0 ** -126, 3e-39, 0.3])
     _both_forms(x, u, "t p", t=[1e-40, 1e-20, 1e38, 5.0, 1e-3, 0.3], p=0.9)
     _both_forms(x, u, "t k", t=[inf, 1e-20, 1e38, 5.0, 1e-3, 0.3], k=700)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_the_longest_row(dt):
+    # equal logits, u a whole number of 1 / V: exactly token u V, and of the lower half with p = 1/2
+    V = 1 << 24
+    x = torch.zeros(1, V, dtype=dt, device=DEV)
+    for n in (0, 1, 12345679, V - 2, V - 1):
+        assert _both_forms(x, [n / V], str(n), oracle=False)[0] == [n]
+        tok, lp = _both_forms(x, [n / V], str(n), oracle=False, p=0.5)
+        assert tok == [n // 2] and abs(lp[0] + 23 * math.log(2)) < 1e-5
+    assert _both_forms(x, [0.75], "k", oracle=False, k=V - 4)[0] == [V // 4 * 3 - 3]
+    x[0, V - 3] = 1.0
+    assert _both_forms(x, [0.99], "greedy", oracle=False, t=0.0)[0] == [V - 3]
+
+
+def test_the_most_rows_and_far_ones():
+    R = 1 << 20
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    u = torch.rand(R, generator=g, device=DEV)
+    tok, lp = rtopk.sample_filtered(torch.zeros(R, 2, dtype=F16, device=DEV), u)
+    torch.cuda.synchronize()
+    assert torch.equal(tok, (u >= 0.5).int()) and ((lp + math.log(2)).abs() < 1e-6).all()
+    far = torch.zeros((1 << 31) + 30008, dtype=F16, device=DEV)  # the second row's offset passes 32 bits
+    x = torch.as_strided(far, (2, 30000), (1 << 31, 1))
+    x.copy_(_rows(2, 30000, F16, seed=31)[0])
+    for kw in (dict(k=30, p=0.9), dict(p=0.99), dict()):
+        assert _both_forms(x, [0.3, 0.8], "far", oracle=False, **kw) == _check(x.contiguous(), [0.3, 0.8], "near", **kw)
