@@ -18,6 +18,7 @@
 #include <cmath>
 
 #include "rtopk_filter.h"
+#include "rtopk_rows.h"
 
 namespace rtopk {
 namespace {
@@ -30,8 +31,6 @@ constexpr int kWaveList = kList / kFWaves;
 constexpr int kZone = 2 * kFThreads; // logits around the borders that are ordered one by one, at most
 
 typedef uint32_t f_u32x4 __attribute__((ext_vector_type(4)));
-typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-constexpr int kSortStep = 16; // logits of the zone that are on their way together
 
 // Logits as they are stored: raw bits, and how many 16 bytes hold.
 template <int DT> struct Logit;
@@ -85,22 +84,33 @@ struct Weigh {
 };
 static_assert(kSteps == 1 << 9, "m / kSteps goes to bit 52");
 
-template <typename T> __device__ __forceinline__ T wave_sum(T x)
+// x of the lane that DPP control CTRL names, 0 where it names none or ROWS leaves the row of 16 out
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t x)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        x += __shfl_xor(x, o);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x)
+{
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(x >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)x);
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t x, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)x, lane); }
+__device__ __forceinline__ uint64_t of_lane(uint64_t x, int lane)
+{
+    return (uint64_t)of_lane((uint32_t)(x >> 32), lane) << 32 | of_lane((uint32_t)x, lane);
+}
+// Sums over the lanes up to each and over all; every lane runs. (By exchanges through LDS a sum's six steps took
+// 0.4 us, and a row waits for eight of them.)
+template <typename T> __device__ __forceinline__ T scan_up(T x)
+{
+    x += moved<0x111, 0xf>(x); // the lane below in the row of 16, then 2, 4 and 8 below
+    x += moved<0x112, 0xf>(x);
+    x += moved<0x114, 0xf>(x);
+    x += moved<0x118, 0xf>(x);
+    x += moved<0x142, 0xa>(x); // the last lane of the row below, for rows 1 and 3
+    x += moved<0x143, 0xc>(x); // lane 31, for rows 2 and 3
     return x;
 }
-template <typename T> __device__ __forceinline__ T scan_up(T x, int lane) // inclusive
-{
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const T y = __shfl_up(x, o);
-        x += lane >= o ? y : 0;
-    }
-    return x;
-}
+template <typename T> __device__ __forceinline__ T wave_sum(T x) { return of_lane(scan_up(x), 63); }
 
 // What a workgroup keeps in LDS.
 struct Shared {
@@ -109,8 +119,7 @@ struct Shared {
         uint64_t w[kBins + 64]; // weights by bins, and the last bin's by lanes
         uint32_t n[kBins + 64]; // or counts
     };
-    alignas(16) uint64_t zone[kZone];
-    uint64_t sorted[kZone];
+    uint64_t zone[kZone], parts[kZone];
     uint32_t list[kFWaves][kWaveList]; // tokens
     uint64_t scan[kFWaves];
     float2 ends[kFWaves];
@@ -154,6 +163,8 @@ template <int DT, bool SHORT> struct RowFilter {
     int from, to;   // the pieces that this workgroup reads
     int mine;       // length of this wave's list, -1: none
     int shift;      // a run is 2^shift pieces: kBins runs hold the row
+    f_u32x4 ready;  // piece ready_at, loaded ahead
+    int ready_at;
 
     __device__ __forceinline__ RowFilter(const FilterArgs &args, Shared &shared, int r) : a(args), sh(shared), row(r)
     {
@@ -167,7 +178,7 @@ template <int DT, bool SHORT> struct RowFilter {
         base = (const __attribute__((address_space(1))) f_u32x4 *)((uintptr_t)x & ~(uintptr_t)15);
         from = 0;
         to = pieces;
-        mine = -1;
+        mine = ready_at = -1;
         shift = 0;
         while ((pieces - 1) >> shift >= kBins)
             ++shift;
@@ -191,7 +202,11 @@ template <int DT, bool SHORT> struct RowFilter {
     // piece i, with -infinity in the place of what is not the row's
     __device__ __forceinline__ f_u32x4 piece(int i) const
     {
-        f_u32x4 v = base[i];
+        f_u32x4 v;
+        if (SHORT && i == ready_at)
+            v = ready;
+        else
+            v = base[i];
         if (i == 0 || i == pieces - 1) {
             constexpr uint32_t none = sizeof(Raw) == 4 ? 0xff800000u : DT == 1 ? 0xfc00u : 0xff80u;
 #pragma unroll
@@ -259,11 +274,12 @@ template <int DT, bool SHORT> struct RowFilter {
     }
     __device__ __forceinline__ void all_range(float &x, float &y) // of the workgroup
     {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            x = fmaxf(x, __shfl_xor(x, o));
-            y = fminf(y, __shfl_xor(y, o));
-        }
+        x = __uint_as_float(group_all<64>(__float_as_uint(x), [](uint32_t p, uint32_t q) {
+            return __float_as_uint(fmaxf(__uint_as_float(p), __uint_as_float(q)));
+        }));
+        y = __uint_as_float(group_all<64>(__float_as_uint(y), [](uint32_t p, uint32_t q) {
+            return __float_as_uint(fminf(__uint_as_float(p), __uint_as_float(q)));
+        }));
         __syncthreads();
         if (lane == 0)
             sh.ends[wave] = make_float2(x, y);
@@ -357,7 +373,7 @@ template <int DT, bool SHORT> struct RowFilter {
     // The sum over the threads before this one.
     __device__ __forceinline__ uint64_t before_me(uint64_t x)
     {
-        const uint64_t upto = scan_up(x, lane);
+        const uint64_t upto = scan_up(x);
         __syncthreads();
         if (lane == 63)
             sh.scan[wave] = upto;
@@ -567,9 +583,9 @@ template <int DT, bool SHORT> struct RowFilter {
         } else if (by_k || by_p) {
             const int kept = kept_of_zone(b, (int)sh.count);
             if (kept > 0)
-                cut = sh.sorted[kept - 1];
+                cut = sh.zone[kept - 1];
             for (int i = tid; i < kept; i += kFThreads) {
-                const uint64_t o = sh.sorted[i], w = weigh(value_of(o));
+                const uint64_t o = sh.zone[i], w = weigh(value_of(o));
                 add_to_run((token_of(o) + lead) / PER, w >= least ? w : 0);
             }
             __syncthreads();
@@ -593,11 +609,7 @@ template <int DT, bool SHORT> struct RowFilter {
             }
         });
         // lanes whose pieces end earlier have missed the last hits
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const int y = __shfl_xor(n, o);
-            n = y > n ? y : n;
-        }
+        n = (int)group_max<64>((uint32_t)n);
         __syncthreads();
         if (tid == 0)
             sh.count = 0;
@@ -616,46 +628,53 @@ template <int DT, bool SHORT> struct RowFilter {
             f(t, at(t));
         }
     }
-    // The zone in its order, by counting: every logit's place is the number of larger ones (455 of them: 5 us;
-    // 2 us at 100).
-    template <int EACH> __device__ __forceinline__ void place_zone(int n)
-    {
-        uint64_t o[EACH];
-        int rank[EACH] = {};
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            o[i] = tid + i * kFThreads < n ? sh.zone[tid + i * kFThreads] : 0;
-        const u64x2 *from = reinterpret_cast<const u64x2 *>(sh.zone);
-        for (int j = 0; j < n; j += kSortStep) {
-            u64x2 y[kSortStep / 2];
-#pragma unroll
-            for (int q = 0; q < kSortStep / 2; ++q)
-                y[q] = from[j / 2 + q];
-#pragma unroll
-            for (int q = 0; q < kSortStep / 2; ++q)
-#pragma unroll
-                for (int i = 0; i < EACH; ++i)
-                    rank[i] += (int)(y[q][0] > o[i]) + (int)(y[q][1] > o[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            if (tid + i * kFThreads < n)
-                sh.sorted[rank[i]] = o[i];
-    }
+    // The zone in its order. A wave orders 64 logits by counting the larger ones of them; a logit's place is the
+    // number of larger ones in all such parts, eight of which are searched together, by halves. (Counting
+    // over the whole zone: 8 us for 480 logits.) Short loops, as above.
     __device__ __forceinline__ void sort_zone(int n)
     {
-        // (padded with zeros to whole steps, which are below every logit)
-        if (tid < kSortStep && n + tid < kZone)
-            sh.zone[n + tid] = 0;
+        constexpr int PARTS = 8, STEP = 16;
+        static_assert(kZone % (64 * PARTS) == 0 && 64 * PARTS % kFThreads == 0, "whole groups of parts");
+        const int filled = n <= 64 ? 64 : (n + 64 * PARTS - 1) & ~(64 * PARTS - 1);
+        uint64_t *to = n <= 64 ? sh.zone : sh.parts;
         __syncthreads();
-        static_assert(kZone == 2 * kFThreads, "two logits per thread");
-        if (n > kFThreads)
-            place_zone<2>(n);
-        else if (wave * 64 < n)
-            place_zone<1>(n);
+#pragma unroll 1
+        for (int first = wave * 64; first < filled; first += kFThreads) {
+            const uint64_t o = first + lane < n ? sh.zone[first + lane] : 0; // below every logit
+            int larger = 0;
+#pragma unroll 1
+            for (int j = 0; first + j < n && j < 64; j += STEP)
+#pragma unroll
+                for (int e = 0; e < STEP; ++e) // (behind the last: 0)
+                    larger += of_lane(o, j + e) > o;
+            to[first + (o ? larger : lane)] = o; // (behind the last in their own places)
+        }
+        __syncthreads();
+        if (n <= 64)
+            return;
+#pragma unroll 1
+        for (int first = wave * 64; first < n; first += kFThreads) {
+            const uint64_t o = sh.parts[first + lane];
+            int place = 0;
+#pragma unroll 1
+            for (int q = 0; q < n; q += 64 * PARTS) {
+                const uint64_t *part = sh.parts + q;
+                uint32_t larger[PARTS] = {};
+#pragma unroll 1
+                for (uint32_t by = 32; by > 0; by >>= 1)
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c)
+                        larger[c] += part[64 * c + larger[c] + by - 1] > o ? by : 0;
+#pragma unroll
+                for (int c = 0; c < PARTS; ++c) // up to 63 so far
+                    place += (int)larger[c] + (part[64 * c + larger[c]] > o);
+            }
+            if (o)
+                sh.zone[place] = o;
+        }
         __syncthreads();
     }
-    // How many of the n logits of the zones top-k and top-p keep; sh.sorted is the zone in its order.
+    // How many of the n logits of the zones top-k and top-p keep; sh.zone is in its order then.
     __device__ __forceinline__ int kept_of_zone(const Borders &b, int n)
     {
         constexpr int EACH = kZone / kFThreads;
@@ -667,7 +686,7 @@ template <int DT, bool SHORT> struct RowFilter {
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int at = tid * EACH + i;
-            const float x = at < n ? value_of(sh.sorted[at]) : -INFINITY;
+            const float x = at < n ? value_of(sh.zone[at]) : -INFINITY;
             w[i] = at < n ? weigh(x) : 0;
             above += at < n && bin(x) < b.kb;
             sum += w[i];
@@ -742,7 +761,7 @@ template <int DT, bool SHORT> struct RowFilter {
                 x = order(y, t + lane) >= cut ? weigh(y) : 0;
                 x = x >= least ? x : 0;
             }
-            const uint64_t upto = c + scan_up(x, lane);
+            const uint64_t upto = c + scan_up(x);
             const uint64_t hit = __ballot(upto > goal);
             if (hit) {
                 if (lane == __ffsll((unsigned long long)hit) - 1) {
@@ -751,7 +770,7 @@ template <int DT, bool SHORT> struct RowFilter {
                 }
                 return;
             }
-            c = __shfl(upto, 63);
+            c = of_lane(upto, 63);
         }
     }
     // The first token of its pieces that has the largest logit (~0: none), for thread 0.
@@ -759,11 +778,7 @@ template <int DT, bool SHORT> struct RowFilter {
     {
         uint32_t first = ~0u;
         each(from, to, tid, kFThreads, [&](int t, float x) { first = x == top && (uint32_t)t < first ? (uint32_t)t : first; });
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const uint32_t y = __shfl_xor(first, o);
-            first = y < first ? y : first;
-        }
+        first = ~group_max<64>(~first);
         __syncthreads();
         if (lane == 0)
             sh.part32[wave] = first;
@@ -856,13 +871,13 @@ template <int DT, bool SHORT> struct RowFilter {
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
                     own += i < p1 && value(q, e) == v;
-                const uint32_t upto = scan_up(own, lane);
+                const uint32_t upto = scan_up(own);
                 uint64_t at = before + upto - own; // ties in front
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
                     if (i < p1 && value(q, e) == v && ++at == ties)
                         sh.value[3] = order(v, i * PER + e - lead);
-                before += __shfl(upto, 63);
+                before += of_lane(upto, 63);
             }
         }
         __syncthreads();
@@ -935,6 +950,8 @@ static_assert(sizeof(SplitRow) == kFilterRowBytes, "rtopk_filter.h");
 __device__ __forceinline__ void put64(uint64_t *p, uint64_t x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t get64(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
+// The chunk of a workgroup. Few rows wait for memory more than for anything else: what a launch reads is on
+// its way together, its first pieces among it.
 template <int DT> __device__ __forceinline__ void take_chunk(RowFilter<DT, true> &f, int chunk, int chunks)
 {
     const int runs = ((f.pieces - 1) >> f.shift) + 1, per = (runs + chunks - 1) / chunks;
@@ -942,6 +959,8 @@ template <int DT> __device__ __forceinline__ void take_chunk(RowFilter<DT, true>
     f.from = f.from < f.pieces ? f.from : f.pieces;
     f.to = ((chunk + 1) * per) << f.shift;
     f.to = f.to < f.pieces ? f.to : f.pieces;
+    f.ready_at = f.from + f.tid < f.pieces ? f.from + f.tid : f.pieces - 1;
+    f.ready = f.base[f.ready_at];
 }
 
 template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_range(const FilterArgs a, SplitRow *rows, int chunks)
@@ -1011,6 +1030,14 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
     RowFilter<DT, true> f(a, sh, row);
     take_chunk(f, chunk, chunks);
     SplitRow &s = rows[row];
+    constexpr int EACH = kBins / kFThreads;
+    uint32_t counts[EACH];
+    uint64_t weights[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        counts[i] = s.n[f.tid + i * kFThreads];
+        weights[i] = s.w[f.tid + i * kFThreads];
+    }
     float hi, lo;
     row_range(f, s, chunks, hi, lo);
     if (hi == -INFINITY) {
@@ -1027,16 +1054,17 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
     } else {
         __syncthreads(); // the table
         if (f.by_k) {
-            f.clear_bins();
-            for (int i = f.tid; i < kBins; i += kFThreads)
-                sh.n[i] = s.n[i];
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                sh.n[f.tid + i * kFThreads] = counts[i];
             __syncthreads();
             f.border_of_count(b, 0);
         }
         if (f.by_p) {
             __syncthreads();
-            for (int i = f.tid; i < kBins; i += kFThreads)
-                sh.w[i] = s.w[i];
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                sh.w[f.tid + i * kFThreads] = weights[i];
             __syncthreads();
             f.border_of_weight(b);
         }
@@ -1070,10 +1098,19 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_draw(co
         return;
     }
     const int runs = ((f.pieces - 1) >> f.shift) + 1;
-    for (int i = f.tid; i < kBins; i += kFThreads)
-        sh.w[i] = i < runs ? get64(&s.runs[i]) : 0;
-    for (int i = f.tid; i < kZone; i += kFThreads) // (what lies behind the zone's logits is not used)
-        sh.zone[i] = get64(&s.zone[i]);
+    uint64_t zone[kZone / kFThreads];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        weights[i] = get64(&s.runs[f.tid + i * kFThreads]);
+#pragma unroll
+    for (int i = 0; i < kZone / kFThreads; ++i) // (what lies behind the zone's logits is not used)
+        zone[i] = get64(&s.zone[f.tid + i * kFThreads]);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        sh.w[f.tid + i * kFThreads] = f.tid + i * kFThreads < runs ? weights[i] : 0;
+#pragma unroll
+    for (int i = 0; i < kZone / kFThreads; ++i)
+        sh.zone[f.tid + i * kFThreads] = zone[i];
     if (f.tid == 0)
         sh.count = __hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     f.from = 0;

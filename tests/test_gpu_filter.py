@@ -311,3 +311,19 @@ def test_the_most_rows_and_far_ones():
     x.copy_(_rows(2, 30000, F16, seed=31)[0])
     for kw in (dict(k=30, p=0.9), dict(p=0.99), dict()):
         assert _both_forms(x, [0.3, 0.8], "far", oracle=False, **kw) == _check(x.contiguous(), [0.3, 0.8], "near", **kw)
+
+
+@pytest.mark.parametrize("n", [2, 63, 64, 65, 130, 511, 512, 513, 700, 1023, 1024, 1025, 1500])
+def test_borders_in_a_cluster(n):
+    # n distinct logits in one of the bins that a row is cut into: their order decides
+    rng = np.random.default_rng(n)
+    for V in (6000, 30000):
+        x = (-5 - 15 * rng.random((3, V))).astype(np.float32)
+        for r in range(3):
+            at = rng.permutation(V)[:n + 2]
+            x[r, at] = 1 + np.arange(n + 2, dtype=np.float32) * np.float32(2.0 ** -22)
+            x[r, at[0]], x[r, at[1]] = 3.0, -40.0
+        x = torch.tensor(x, device=DEV)
+        u = rng.random(3)
+        for kw in (dict(k=1 + n // 3), dict(k=n), dict(k=1 + n), dict(p=0.31), dict(p=0.9), dict(k=1 + n // 2, p=0.77), dict(k=n, p=0.5, m=0.1)):
+            _both_forms(x, u, f"{V} {kw}", **kw)
