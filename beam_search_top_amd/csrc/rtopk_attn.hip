@@ -516,7 +516,10 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
     };
 
     // ---- loads of an 8-bit cache: to registers, a lane 16 codes of one key, a wave 1 KiB
-    // a load; a step later they go to LDS as numbers of the type of q, 2 chunks each.
+    // a load; a step later they go to LDS as numbers of the type of q, 2 chunks each. So the
+    // products and their operands are those of a 16-bit cache, and a tile is decoded once for all rows. 32 requests
+    // of 64 nodes over 1500-4000 keys, 32/8 heads of 128: 165 us (a 16-bit cache: 157), of equal lengths
+    // 126: the longest request's workgroup decides. Four waves, two workgroups to a CU, decode every tile twice: 189 us.
     constexpr int CH8 = DP / 16, RPL8 = 64 / CH8, NI8 = BN / RPL8 / WR > 0 ? BN / RPL8 / WR : 1;
     struct Codes {
         u32x4 c[NI8];
@@ -933,9 +936,10 @@ __device__ __forceinline__ uint64_t get64(const void *p)
 
 constexpr int kFewWaves = 4;
 // Workgroups per CU that the registers of attn_few have to leave room for. 8 bits, one row: with heads of 64 three
-// (2 requests of 90000 and 131000 keys of 16 heads: 134 us, with four, which spill, 153); with heads of 128 two (8
-// heads: 98 us, three, which spill, 103).
-constexpr int few_waves(int dp, int nb) { return kF8 && nb == 1 && dp == 64 ? 3 : 2; }
+// (2 requests of 90000 and 131000 keys of 16 heads, steps of 32 keys: 134 us, with four, which spill, 153), but two where every lane has an offset of
+// its own (pages of 24: 129 us, with three, which spill, 133); with heads of 128 two (8 heads: 98 us, 4.7 TB/s; three, which
+// spill, 103).
+constexpr int few_waves(int dp, int nb, int mode) { return kF8 && nb == 1 && dp == 64 && mode != 2 ? 3 : 2; }
 // Keys per step of a wave. 64 of 64 codes: half as many bytes on their way were too few (2 x 440000 keys of 16
 // heads: 414 us, with 32 500 us; with 128 codes 64 make no difference, and two blocks of rows spill).
 constexpr int few_step(int dp) { return kF8 && dp == 64 ? 64 : 32; }
@@ -1014,7 +1018,7 @@ template <bool TREE, int kFewStep> __device__ __forceinline__ Share find_share(c
 // tokens; 2: a tree, other pages. (Modes of one kernel, not branches in it: the counts by which a wave waits for
 // its older loads only must be the same on every path.)
 template <int DT, int DP, int NB, int MODE>
-__global__ __launch_bounds__(64 * kFewWaves, few_waves(DP, NB)) void attn_few(const Args a)
+__global__ __launch_bounds__(64 * kFewWaves, few_waves(DP, NB, MODE)) void attn_few(const Args a)
 {
     constexpr bool TREE = MODE != 0;
     constexpr int kFewStep = few_step(DP), GROUPS = kFewStep / 32; // keys of a step, products with the values over them

@@ -8,9 +8,16 @@
 
 using rtopk::set_error;
 
+extern "C" size_t rtopk_sample_filtered_workspace_bytes(int R, int V)
+{
+    if (R < 1 || V < 1 || V > rtopk::kFilterMaxV || R > rtopk::kFilterMaxR)
+        return 0;
+    return rtopk::kWsFixedBytes + (rtopk::filter_chunks(R, V) > 1 ? R * rtopk::kFilterRowBytes : 0);
+}
+
 extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
                                      const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
-                                     int32_t *out_token, float *out_logprob, void *stream)
+                                     int32_t *out_token, float *out_logprob, void *workspace, size_t ws_bytes, void *stream)
 {
     const char *what = "filtered sampling";
     if (!logits || !u || !out_token || !out_logprob)
@@ -26,6 +33,11 @@ extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V
     if (V > rtopk::kFilterMaxV || R > rtopk::kFilterMaxR)
         return set_error(RTOPK_ENOTSUP, "%s: V=%d or R=%d exceeds the implementation limits %d and %d", what, V, R,
                          rtopk::kFilterMaxV, rtopk::kFilterMaxR);
+    if (workspace && (uintptr_t)workspace % 256)
+        return set_error(RTOPK_EINVAL, "%s: workspace is not 256-byte aligned", what);
+    const size_t need = rtopk_sample_filtered_workspace_bytes(R, V);
+    if (workspace && ws_bytes < need)
+        return set_error(RTOPK_ENOMEM, "%s: workspace of %zu bytes is below the %zu needed", what, ws_bytes, need);
     rtopk::FilterArgs a{};
     a.logits = logits;
     a.R = R;
@@ -46,6 +58,8 @@ extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V
         return (int)RTOPK_OK;
     };
     const int chunks = rtopk::filter_chunks(R, V);
+    if (chunks > 1 && workspace)
+        return go(chunks, (uint8_t *)workspace + rtopk::kWsFixedBytes);
     if (chunks > 1) {
         // a captured launch would keep the address of a workspace that a later call may free: it takes
         // the form without one
@@ -55,7 +69,6 @@ extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V
             return set_error(RTOPK_EHIP, "%s: hipStreamIsCapturing: %s", what, hipGetErrorString(e));
         if (cap == hipStreamCaptureStatusNone)
             try {
-                const size_t need = rtopk::kWsFixedBytes + R * rtopk::kFilterRowBytes;
                 return rtopk::with_workspace(need, (hipStream_t)stream,
                                              [&](void *ws) { return go(chunks, (uint8_t *)ws + rtopk::kWsFixedBytes); });
             } catch (const std::exception &x) { // it must not leave a C entry point

@@ -36,10 +36,10 @@ constexpr int kFilterChunks = 64;
 constexpr size_t kFilterRowBytes = 49920; // workspace of a row that is cut
 inline int filter_chunks(int R, int V)
 {
-    // Three launches and the workspace between them cost about 17 us whatever the size; a row's own workgroup takes
-    // 20 to 40 us per 40000 logits, and leaves CUs idle up to 256 rows. us cut / not: 1 x 16000 18 / 12, 16 x 24000
-    // 30 / 27, 64 x 24000 35 / 29; 1 x 32000 19 / 21, 32 x 32000 27 / 40, 128 x 32000 39 / 41, 128 x 100000 64 / 89,
-    // 8 x 250000 37 / 200; 200 x 40000 55 / 43, 256 x 100000 100 / 90.
+    // Three launches and the workspace between them cost about 15 us whatever the size; a row's own workgroup takes
+    // 20 to 40 us per 40000 logits, and leaves CUs idle up to 256 rows. us cut / not: 1 x 16000 17 / 11, 16 x 24000
+    // 25 / 24, 64 x 24000 34 / 27; 1 x 28672 16 / 17, 32 x 32000 29 / 31, 64 x 40000 35 / 37, 128 x 32000 37 / 38,
+    // 128 x 100000 62 / 81, 8 x 250000 34 / 182; 200 x 40000 53 / 41, 256 x 100000 98 / 82.
     const int most = V / 4096;
     if (R > 128 || most < 7)
         return 1;

@@ -894,6 +894,10 @@ template <int DT, bool SHORT> struct RowFilter {
 //   4. The logits of the bins in which the borders lie are ordered one by one, which gives the cut. A row
 //      with too many equal or nearly equal ones finds it by the bits of the logits.
 //   5. Kept weights are summed by runs of the row, and the run that the draw falls in is read again.
+// 512 rows of 40000, float16, 54.8 us, two rows to a CU. Bound by the vector unit in the rows that have top-p alone and
+// keep more than a list holds: two passes of about 30 instructions per logit, 13 to 20 us each while two rows
+// share the CU; such a row takes 53 us, one with top-k 27 (its count waits for LDS atomics, 6.5). A list of twice the
+// length would save nothing: making and reading it takes 15 us, a whole pass 17. Loads three pieces ahead spill: 63 us.
 template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(const FilterArgs a)
 {
     __shared__ Shared sh;
@@ -937,7 +941,9 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(con
 }
 
 // ---- few rows: each cut into `chunks` of whole runs, a workgroup each, in three launches that pass
-// histograms, sums and zones through the workspace.
+// histograms, sums and zones through the workspace. 8 rows of 250000, bfloat16, 33 us: 3, 9 and 19 of the launches and
+// their gaps; 32 rows of 32000, float32, 25.6. Bound by chains of round trips (ends, histograms, ticket, runs, the
+// drawn run) and by code that every workgroup fetches cold.
 struct alignas(256) SplitRow {
     uint64_t w[kBins], runs[kBins], zone[kZone];
     uint32_t n[kBins];

@@ -117,8 +117,10 @@ def load():
     L.rtopk_tree_attention_fp8.restype = i32
     L.rtopk_tree_attention_fp8_workspace_bytes.argtypes = [i32] * 7
     L.rtopk_tree_attention_fp8_workspace_bytes.restype = sz
-    L.rtopk_sample_filtered.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.rtopk_sample_filtered.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.rtopk_sample_filtered.restype = i32
+    L.rtopk_sample_filtered_workspace_bytes.argtypes = [i32] * 2
+    L.rtopk_sample_filtered_workspace_bytes.restype = sz
     L.rtopk_read_probe.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
     L.rtopk_read_probe.restype = i32
     L.rtopk_read_probe_shape.argtypes = [vp, sz, i32, i32, ctypes.c_uint32, vp, vp]
@@ -363,9 +365,14 @@ def rtopk_tree_attention_fp8_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page):
     return load().rtopk_tree_attention_fp8_workspace_bytes(B, N, Hq, Hkv, D, table_ld, page)
 
 
-def rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token, out_logprob, stream):
+def rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token, out_logprob, workspace,
+                          ws_bytes, stream):
     return load().rtopk_sample_filtered(logits, dtype, R, V, ld, temperature, top_k, top_p, min_p, u, out_token,
-                                        out_logprob, stream)
+                                        out_logprob, workspace, ws_bytes, stream)
+
+
+def rtopk_sample_filtered_workspace_bytes(R, V):
+    return load().rtopk_sample_filtered_workspace_bytes(R, V)
 
 
 def rtopk_read_probe(src, nbytes, marker, out, stream):
@@ -795,13 +802,15 @@ def _row_values(t, R, dtype, dev, name):
     return t.data_ptr()
 
 
-def sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+def sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, workspace=None):
     """Sampling of every row of logits [R, V] with filters, from given random numbers, on the current stream.
 
     logits float32/float16/bfloat16, rows any distance apart; u [R] float32 in
     [0, 1); temperature, top_p, min_p [R] float32 and top_k [R] int32, each None for none:
     a row's k best, of those the shortest beginning with top_p of their weight, of those the ones with
-    min_p of the largest weight. ``out`` may supply the two results. Returns
+    min_p of the largest weight. ``out`` may supply the two results. ``workspace`` (uint8, of
+    rtopk_sample_filtered_workspace_bytes(R, V) bytes) lets few long rows be cut over workgroups under
+    graph capture too; calls that share one must be ordered. Returns
     (tokens [R] int32, logprobs [R] float32 under what is kept).
     """
     torch = _get_torch()
@@ -820,11 +829,15 @@ def sample_filtered(logits, u, temperature=None, top_k=None, top_p=None, min_p=N
             raise ValueError("out must hold two tensors (tokens, logprobs)")
         tok, lp = out
     f32 = torch.float32
+    wp, wn = None, 0
+    if workspace is not None:
+        _check_workspace(workspace, logits.device, 0)
+        wp, wn = workspace.data_ptr(), workspace.numel()
     _enqueue(dev, load().rtopk_sample_filtered, logits.data_ptr(), _code(logits), R, V, st[0],
              _row_values(temperature, R, f32, dev, "temperature"), _row_values(top_k, R, torch.int32, dev, "top_k"),
              _row_values(top_p, R, f32, dev, "top_p"), _row_values(min_p, R, f32, dev, "min_p"),
              _row_values(u, R, f32, dev, "u"), _row_values(tok, R, torch.int32, dev, "out tokens"),
-             _row_values(lp, R, f32, dev, "out logprobs"))
+             _row_values(lp, R, f32, dev, "out logprobs"), wp, wn)
     return tok, lp
 
 

@@ -593,13 +593,17 @@ size_t rtopk_tree_attention_fp8_workspace_bytes(int B, int N, int Hq, int Hkv, i
  * 62 - ceil(log2 V)), so that sums are exact and the same call gives the same result;
  * a candidate of weight below 2^-(f+1) is never drawn. The largest float32 counts as
  * infinite. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`. Few
- * long rows are cut over workgroups, which takes three launches and the library-owned
- * workspace that rtopk_cross_attention describes (calls on one stream come from one thread
- * at a time); under graph capture a call takes one launch and none, with the same results.
+ * long rows are cut over workgroups, which takes three launches and a workspace: the caller's, of
+ * ws_bytes >= rtopk_sample_filtered_workspace_bytes(...) bytes and 256-byte aligned (it needs no
+ * filling; calls sharing it must be ordered), or with NULL the library-owned one that
+ * rtopk_cross_attention describes (calls on one stream come from one thread at a time). A
+ * captured call without the caller's workspace takes one launch and none, with the same
+ * results but more time.
  */
 int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
-                          int32_t *out_token, float *out_logprob, void *stream);
+                          int32_t *out_token, float *out_logprob, void *workspace, size_t ws_bytes, void *stream);
+size_t rtopk_sample_filtered_workspace_bytes(int R, int V); /* 0 on bad arguments */
 
 /*
  * Measurement aid, not part of the selection: a plain streaming read that

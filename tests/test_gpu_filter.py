@@ -190,7 +190,7 @@ def test_agrees_with_the_top_k_step():
 
 
 def _both_forms(x, u, what, oracle=True, **f):
-    """Few long rows are cut over workgroups, but not in a captured call: both give the same."""
+    """Few long rows are cut over workgroups, but not in a captured call without a workspace: all give the same."""
     R = x.shape[0]
     d = lambda a, dt: None if a is None else torch.tensor([a] * R if np.isscalar(a) else a, dtype=dt, device=DEV)  # noqa: E731
     ud = torch.tensor(np.asarray(u, dtype=np.float32), device=DEV)
@@ -199,11 +199,17 @@ def _both_forms(x, u, what, oracle=True, **f):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         rtopk.sample_filtered(x, ud, out=out, **kw)
+    cut = (torch.zeros(R, dtype=torch.int32, device=DEV), torch.zeros(R, device=DEV))
+    ws = torch.full((rtopk.rtopk_sample_filtered_workspace_bytes(*x.shape),), 0xa5, dtype=torch.uint8, device=DEV)
+    given = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(given):
+        rtopk.sample_filtered(x, ud, out=cut, workspace=ws, **kw)
     eager = rtopk.sample_filtered(x, ud, **kw)
     graph.replay()
+    given.replay()
     torch.cuda.synchronize()
-    one, other = [[t.tolist() for t in pair] for pair in (out, eager)]
-    assert one == other, what
+    one, other, third = [[t.tolist() for t in pair] for pair in (out, eager, cut)]
+    assert one == other == third, what
     return _check(x, u, what, **f) if oracle else tuple(other)
 
 
@@ -327,3 +333,33 @@ def test_borders_in_a_cluster(n):
         u = rng.random(3)
         for kw in (dict(k=1 + n // 3), dict(k=n), dict(k=1 + n), dict(p=0.31), dict(p=0.9), dict(k=1 + n // 2, p=0.77), dict(k=n, p=0.5, m=0.1)):
             _both_forms(x, u, f"{V} {kw}", **kw)
+
+
+def test_replays_with_a_workspace():
+    # two captured calls that share one workspace, in order, over inputs that change
+    x, rng = _rows(5, 60000, BF16, seed=41)
+    y, _ = _rows(3, 100000, F16, seed=42)
+    u = torch.tensor(rng.random(5), dtype=F32, device=DEV)
+    p = torch.full((5,), 0.9, device=DEV)
+    n = max(rtopk.rtopk_sample_filtered_workspace_bytes(*z.shape) for z in (x, y))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    outs = [(torch.zeros(len(z), dtype=torch.int32, device=DEV), torch.zeros(len(z), device=DEV)) for z in (x, y)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for z, o in zip((x, y), outs):
+            rtopk.sample_filtered(z, u[:len(z)], top_p=p[:len(z)], out=o, workspace=ws)
+    for i in range(4):
+        u.copy_(torch.tensor(rng.random(5)))
+        x.neg_()
+        y.mul_(0.8)
+        graph.replay()
+        torch.cuda.synchronize()
+        for z, o in zip((x, y), outs):
+            want = rtopk.sample_filtered(z, u[:len(z)], top_p=p[:len(z)])
+            assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1]), i
+    with pytest.raises(rtopk.RtopkError):
+        rtopk.sample_filtered(x, u, workspace=ws[:1000])
+    with pytest.raises(ValueError):
+        rtopk.sample_filtered(x, u, workspace=ws.view(torch.int8))
+    with pytest.raises(ValueError):
+        rtopk.sample_filtered(x, u, workspace=torch.empty(n, dtype=torch.uint8))

@@ -147,7 +147,7 @@ def test_load_refusals(lib, kw, status, msg):
     assert st == status and msg in err, err
 
 
-FILTER = dict(logits=FAKE, dtype=1, R=4, V=100, ld=100, t=None, k=None, p=None, m=None, u=FAKE, tok=FAKE, lp=FAKE, stream=None)
+FILTER = dict(logits=FAKE, dtype=1, R=4, V=100, ld=100, t=None, k=None, p=None, m=None, u=FAKE, tok=FAKE, lp=FAKE, ws=None, nws=0, stream=None)
 
 
 @pytest.mark.parametrize("kw,status,msg", [
@@ -155,10 +155,18 @@ FILTER = dict(logits=FAKE, dtype=1, R=4, V=100, ld=100, t=None, k=None, p=None, 
     (dict(dtype=3), E, "dtype"), (dict(R=0), E, "sizes"), (dict(V=0), E, "sizes"), (dict(ld=99), E, "rows"), (dict(ld=-1, R=1), E, "rows"),
     (dict(ld=2 ** 41), E, "rows"), (dict(logits=FAKE + 1), E, "aligned"), (dict(logits=FAKE + 2, dtype=0), E, "aligned"),
     (dict(V=2 ** 24 + 1, ld=2 ** 25), N, "limit"), (dict(R=2 ** 20 + 1), N, "limit"),
+    (dict(ws=FAKE + 16, nws=1 << 30), E, "256-byte"), (dict(ws=FAKE, nws=100), rtopk.RTOPK_ENOMEM, "workspace"),
+    (dict(ws=FAKE, nws=49920 * 4, V=50000, ld=50000), rtopk.RTOPK_ENOMEM, "workspace"),
 ])
 def test_filter_refusals(lib, kw, status, msg):
     st, err = _call(rtopk.rtopk_sample_filtered, FILTER, kw)
     assert st == status and msg in err, err
+
+
+def test_filter_workspace_sizes(lib):
+    assert all(rtopk.rtopk_sample_filtered_workspace_bytes(*s) == 0 for s in ((0, 5), (5, 0), (1, 2 ** 24 + 1), (2 ** 20 + 1, 5)))
+    few, long, many = (rtopk.rtopk_sample_filtered_workspace_bytes(*s) for s in ((8, 1000), (8, 250000), (2 ** 20, 2 ** 24)))
+    assert 0 < few < long and many == few
 
 
 def test_host_tensors_are_refused(lib):
