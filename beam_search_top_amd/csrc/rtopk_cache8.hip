@@ -58,7 +58,7 @@ template <int DT, int LPH> struct Quantise {
 // A workgroup takes `tpw` tokens; every row (a head of a token) is a group of LPH
 // lanes, 16 elements each, which takes the key's and the value's row together, so that the
 // largest element is found by lane moves alone. Bound by HBM: 130001 tokens of 8 heads of 128, bfloat16, 152 us,
-// 5.25 TB/s read and written; 200 tokens of 16 x 64 3.6 us, the call on the host 8.5.
+// 5.25 TB/s read and written; 200 tokens of 16 x 64 3.6 us, the call on the host 8.
 template <int DT, int LPH> __global__ __launch_bounds__(kC8Threads) void cache8_store(const Cache8Args a)
 {
     typedef Row<DT> X;

@@ -671,11 +671,12 @@ def _cache8(k_cache, v_cache, k_scales, v_scales, dev):
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape or k_cache.stride() != v_cache.stride():
         raise ValueError("k_cache and v_cache must be [pages, page, Hkv, D] tensors of the same strides")
-    codes = (_torch.float8_e4m3fn, _torch.uint8)
-    if k_cache.dtype not in codes or v_cache.dtype is not k_cache.dtype:
+    dt = k_cache.dtype
+    if (dt is not _torch.float8_e4m3fn and dt is not _torch.uint8) or v_cache.dtype is not dt:
         raise ValueError("k_cache and v_cache must be float8_e4m3fn or uint8")
+    rows = shape[:3]
     for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if t.dtype is not _torch.uint8 or t.shape != shape[:3] or not t.is_contiguous():
+        if t.dtype is not _torch.uint8 or t.shape != rows or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 [pages, page, Hkv] tensor")
     if not k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == dev:
         for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scales, "k_scales"), (v_scales, "v_scales")):
@@ -696,18 +697,17 @@ def cache_store_fp8(k, v, slots, k_cache, v_cache, k_scales, v_scales):
     dev = k.get_device()
     if v.get_device() != dev:
         _on_device(v, k.device, "v")
-    if k.dim() < 3 or k.shape != v.shape or k.dtype is not v.dtype:
+    shape = k.shape
+    if len(shape) < 3 or v.shape != shape or k.dtype is not v.dtype:
         raise ValueError("k and v must be [..., Hkv, D] tensors of one shape and type")
-    if slots.shape != k.shape[:-2]:
-        raise ValueError("slots must have the leading shape of k")
-    if k.dim() > 3:
-        k, v = (t.view(-1, *t.shape[-2:]) for t in (k, v))  # raises where the tokens are not evenly strided
     pages, page, Hkv, D = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
-    if k.shape[1:] != (Hkv, D):
+    if shape[-2] != Hkv or shape[-1] != D:
         raise ValueError("k and v must have the cache's heads")
+    at = _ints(slots, shape[:-2], dev, "slots")
+    if len(shape) > 3:
+        k, v = (t.view(-1, Hkv, D) for t in (k, v))  # raises where the tokens are not evenly strided
     _enqueue(dev, load().rtopk_cache_store_fp8, k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), _code(k),
-             _ints(slots, slots.shape, dev, "slots"), k.shape[0], Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(),
-             _strides(k_cache, "k_cache"), k_scales.data_ptr(), v_scales.data_ptr(), pages, page)
+             at, k.size(0), Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), _strides(k_cache, "k_cache"), k_scales.data_ptr(), v_scales.data_ptr(), pages, page)
     return k_cache, v_cache, k_scales, v_scales
 
 
@@ -723,7 +723,8 @@ def cache_load_fp8(k_cache, v_cache, k_scales, v_scales, slots, dtype=None, out=
         raise ValueError("k_cache must be a device tensor")
     dev = k_cache.get_device()
     pages, page, Hkv, D = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
-    shape = slots.shape + (Hkv, D)
+    lead = slots.shape
+    shape = lead + (Hkv, D)
     if out is None:
         dtype = dtype or torch.bfloat16
         k, v = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
@@ -731,14 +732,14 @@ def cache_load_fp8(k_cache, v_cache, k_scales, v_scales, slots, dtype=None, out=
         if len(out) != 2:
             raise ValueError("out must hold two tensors (k, v)")
         k, v = out
-        if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or dtype not in (None, k.dtype) or \
+        if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or (dtype is not None and dtype is not k.dtype) or \
                 not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError(f"out must be two contiguous {list(shape)} tensors of one type")
         if not k.get_device() == v.get_device() == dev:
             _on_device(k, k_cache.device, "out k")
             _on_device(v, k_cache.device, "out v")
     _enqueue(dev, load().rtopk_cache_load_fp8, k_cache.data_ptr(), v_cache.data_ptr(), _strides(k_cache, "k_cache"),
-             k_scales.data_ptr(), v_scales.data_ptr(), pages, page, _ints(slots, slots.shape, dev, "slots"), slots.numel(),
+             k_scales.data_ptr(), v_scales.data_ptr(), pages, page, _ints(slots, lead, dev, "slots"), slots.numel(),
              Hkv, D, k.data_ptr(), v.data_ptr(), _code(k))
     return k, v
 
@@ -764,31 +765,39 @@ def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1e-6,
     if not q.is_cuda:
         raise ValueError("q must be a device tensor")
     dev = q.get_device()
-    lead = q.shape[:-2]
-    if q.dim() < 3 or k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != q.shape[-1] or k.dtype is not q.dtype:
+    qs, ks, dt = q.shape, k.shape, q.dtype
+    lead = qs[:-2]
+    if len(qs) < 3 or ks[:-2] != lead or ks[-1] != qs[-1] or k.dtype is not dt:
         raise ValueError("q and k must be [..., Hq, D] and [..., Hkv, D] tensors of one type")
+    D = qs[-1]
     if freqs.dtype is not torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float32 [rot / 2] tensor")
     if q_out is None:
         # rows of skipped tokens have to hold something: zeros
-        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.zeros(qs, dtype=dt, device=q.device)
+    elif q_out.dtype is not dt or q_out.shape != qs:
+        raise ValueError("q_out must have the shape and type of its input")
     if k_out is None:
-        k_out = torch.zeros(k.shape, dtype=k.dtype, device=q.device)
-    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if t.shape != like.shape or t.dtype is not q.dtype:
-            raise ValueError(f"{name} must have the shape and type of its input")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and (t.dtype is not q.dtype or t.shape != q.shape[-1:] or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous [D] tensor of q's type")
-    for t, name in ((k, "k"), (freqs, "freqs"), (q_out, "q_out"), (k_out, "k_out"), (q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and t.get_device() != dev:
+        k_out = torch.zeros(ks, dtype=dt, device=q.device)
+    elif k_out.dtype is not dt or k_out.shape != ks:
+        raise ValueError("k_out must have the shape and type of its input")
+    weights = [None, None]
+    for i, (t, name) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))):
+        if t is not None:
+            if t.dtype is not dt or t.dim() != 1 or t.numel() != D or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [D] tensor of q's type")
+            if t.get_device() != dev:
+                _on_device(t, q.device, name)
+            weights[i] = t.data_ptr()
+    if not k.get_device() == freqs.get_device() == q_out.get_device() == k_out.get_device() == dev:
+        for t, name in ((k, "k"), (freqs, "freqs"), (q_out, "q_out"), (k_out, "k_out")):
             _on_device(t, q.device, name)
-    q3, k3, qo, ko = _rows3(q, "q"), _rows3(k, "k"), _rows3(q_out, "q_out"), _rows3(k_out, "k_out")
-    T, Hq, D = q3.shape
+    q3, k3, qo, ko = (q, k, q_out, k_out) if len(qs) == 3 else \
+        (_rows3(q, "q"), _rows3(k, "k"), _rows3(q_out, "q_out"), _rows3(k_out, "k_out"))
     _enqueue(dev, load().rtopk_qk_norm_rope, q3.data_ptr(), _strides(q3, "q"), k3.data_ptr(), _strides(k3, "k"), _code(q),
-             _ints(positions, lead, dev, "positions"), freqs.data_ptr(), 2 * freqs.numel(), int(interleaved),
-             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps, T,
-             Hq, k3.shape[1], D, qo.data_ptr(), _strides(qo, "q_out"), ko.data_ptr(), _strides(ko, "k_out"))
+             _ints(positions, lead, dev, "positions"), freqs.data_ptr(), 2 * freqs.numel(), int(interleaved), weights[0],
+             weights[1], eps, q3.size(0), qs[-2], ks[-2], D, qo.data_ptr(), _strides(qo, "q_out"), ko.data_ptr(),
+             _strides(ko, "k_out"))
     return q_out, k_out
 
 
