@@ -252,7 +252,9 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide, 
         // GPU (2 workgroups per CU hold enough loads in flight at D = 128, 4 at D = 64:
         // with 3 and 8 the call above takes 107 and 110 us). 128 x 16 of them are not
         // cut: 34 us, cut in two or more 44 us, for the ends of every share cost more
-        // than the balance gains.
+        // than the balance gains. 8 bits: not cut up to two steps per wave, where shares and their join cost more
+        // (8 requests, 16 heads of 64 / 8 of 128: kernel 8.8 / 8.0 us uncut and 9.4 / 9.5 cut at 500 / 250 keys, 12.7 / 10.9
+        // uncut and 10.3 / 9.9 cut at twice as many).
         p.bn = fp8 && p.dp == 64 ? 64 : 32; // few_step
         p.waves = 4;
         p.row_tiles = 1;
@@ -260,7 +262,7 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide, 
         const int64_t places = p.dp == 64 ? 1024 : 512, tiles = ((int64_t)S + p.bn - 1) / p.bn;
         int64_t units = (places + Hkv - 1) / Hkv;
         units = units > 2 * (int64_t)B ? units : 2 * (int64_t)B;
-        const bool cut = tiles > p.min_tiles && (int64_t)B * Hkv < places && B <= kMaxShareBatch &&
+        const bool cut = tiles > (fp8 ? 2 * p.waves : p.min_tiles) && (int64_t)B * Hkv < places && B <= kMaxShareBatch &&
                          (int64_t)B * tiles <= (1 << 30);
         p.units = cut ? (int)units : 0;
         p.grid = ((cut ? units : B) + 7) / 8 * 8 * Hkv;
