@@ -3,6 +3,7 @@ reference of tree attention (layer_ref.py, which derives the tolerances) on
 what the codes and scales stand for: those values are numbers of the queries' type,
 so that the kernel rounds what it rounds over a cache of that type and nothing more."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -380,3 +381,32 @@ def test_decode_steps_that_sample():
         held = held + new
         new, rows = torch.ones_like(prompts), 1
         tokens = tok[:, None].long()
+
+
+def test_two_threads_with_a_stream_each():
+    # library-owned workspaces are one per stream: calls of two host threads do not meet
+    cases = [_inputs(2, 3, 8, 2, 128, 16, [5000, 300], BF16, seed=s) for s in (81, 82)]
+    logits = [torch.randn(3, 60000, generator=_gen(s), device=DEV).to(BF16) * 2 for s in (83, 84)]
+    u, p = torch.tensor([0.2, 0.5, 0.9], device=DEV), torch.full((3,), 0.9, device=DEV)
+
+    def both(i):
+        return [_call(cases[i])[0], *rtopk.sample_filtered(logits[i], u, top_p=p)]
+
+    want = [both(i) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                got[i].append(both(i))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 30 and all(torch.equal(a, b) for one in got[i] for a, b in zip(one, want[i])), i
