@@ -894,10 +894,12 @@ template <int DT, bool SHORT> struct RowFilter {
 //   4. The logits of the bins in which the borders lie are ordered one by one, which gives the cut. A row
 //      with too many equal or nearly equal ones finds it by the bits of the logits.
 //   5. Kept weights are summed by runs of the row, and the run that the draw falls in is read again.
-// 512 rows of 40000, float16, 54.8 us, two rows to a CU. Bound by the vector unit in the rows that have top-p alone and
-// keep more than a list holds: two passes of about 30 instructions per logit, 13 to 20 us each while two rows
-// share the CU; such a row takes 53 us, one with top-k 27 (its count waits for LDS atomics, 6.5). A list of twice the
-// length would save nothing: making and reading it takes 15 us, a whole pass 17. Loads three pieces ahead spill: 63 us.
+// 512 rows of 40000, float16, 54 us, two rows to a CU. Bound by the rows that have top-p alone and
+// keep more than a list holds: two passes of 25 to 30 vector instructions per logit, 13 us of issue for two rows and
+// 18 to 20 measured; alone on its CU a row's pass takes 11.5 and half of its time is waiting. Such a row takes 52 us,
+// one with top-k 25 (its count, 6, waits for LDS). A list of twice the length would save nothing: making and reading it
+// takes 15 us, a whole pass 17. Loads three pieces ahead spill (63 us), and 1024 threads leave one row to a CU (69 us;
+// with 200 rows 40 against 41).
 template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(const FilterArgs a)
 {
     __shared__ Shared sh;
