@@ -909,14 +909,15 @@ def tree_attention_fp8(q, k_cache, v_cache, k_scales, v_scales, table, cache_len
     [pages, page, Hkv] uint8; everything else as tree_attention (a workspace has
     rtopk_tree_attention_fp8_workspace_bytes(...) bytes). Returns (out, lse)."""
     _get_torch()
-    if not q.is_cuda or q.dim() != 4 or table.dim() != 2:
+    shape, rows = q.shape, table.shape
+    if not q.is_cuda or len(shape) != 4 or len(rows) != 2:
         raise ValueError("q must be a [B, N, Hq, D] device tensor and table [B, ld]")
     dev = q.get_device()
-    B, N, Hq, D = q.shape
+    B, N, Hq, D = shape
     pages, page, Hkv, Dk = _cache8(k_cache, v_cache, k_scales, v_scales, dev)
     if Dk != D:
         raise ValueError("the cache must have q's head size")
-    ld = table.shape[1]
+    ld = rows[1]
     scale, out, lp, wp, wn = _attention_args(q, Hkv, scale, out, lse, workspace, dev)
     _enqueue(dev, load().rtopk_tree_attention_fp8, q.data_ptr(), _strides(q, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
              _strides(k_cache, "k_cache"), k_scales.data_ptr(), v_scales.data_ptr(), _code(q),
