@@ -66,6 +66,10 @@ struct Weigh {
     {
         top = t;
         by = __builtin_fmax(kSteps * 1.4426950408889634 * per_T, 0x1p-900); // T may be infinite
+        // The largest float32 stands for infinity (value()): whatever T, the next number below it, 2^104 away,
+        // weighs nothing beside it.
+        if (t == 0x1.fffffep127)
+            by = __builtin_fmax(by, 200. * kSteps * 0x1p-104);
         low = -200. * kSteps / by;
     }
     __device__ __forceinline__ uint64_t operator()(float x) const
