@@ -78,8 +78,29 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope(const RopeArgs a)
                 sum += x[n][0][e] * x[n][0][e] + x[n][1][e] * x[n][1][e];
         }
         float f = 1.f;
-        if (w)
-            f = 1.f / sqrtf(group_sum<LPH>(sum) / (float)a.D + a.eps);
+        if (w) {
+            const float mean = group_sum<LPH>(sum) / (float)a.D + a.eps;
+            if (mean >= 0x1p-100f && mean <= 0x1.fffffep127f) {
+                f = 1.f / sqrtf(mean);
+            } else {
+                // squares that leave float32's range, or lose bits at its lower end (up to 2^-150 of each, which a
+                // mean of 2^-100 does not feel): the row is normalised in 64 bits, and rounded once on the way
+                double wide = 0.;
+#pragma unroll
+                for (int n = 0; n < NU; ++n)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        wide += (double)x[n][0][e] * x[n][0][e] + (double)x[n][1][e] * x[n][1][e];
+                const double by = 1. / sqrt(group_sum<LPH>(wide) / a.D + (double)a.eps);
+#pragma unroll
+                for (int n = 0; n < NU; ++n)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        x[n][0][e] = (float)(x[n][0][e] * by);
+                        x[n][1][e] = (float)(x[n][1][e] * by);
+                    }
+            }
+        }
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
             const int at = (j + n * LPH) * VE;

@@ -88,6 +88,34 @@ template <int G> __device__ __forceinline__ float group_sum(float x)
         return __float_as_uint(__uint_as_float(p) + __uint_as_float(q));
     }));
 }
+// The same for a sum in 64 bits, whose halves move one after the other.
+template <int CTRL> __device__ __forceinline__ double plus_lane(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return x + __builtin_bit_cast(double, (uint64_t)lane_by<CTRL>((uint32_t)(b >> 32)) << 32 | lane_by<CTRL>((uint32_t)b));
+}
+template <int G> __device__ __forceinline__ double group_sum(double x)
+{
+    const auto halves = [](uint32_t hi, uint32_t lo) { return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo); };
+    x = plus_lane<0x4e>(plus_lane<0xb1>(x));
+    if (G >= 8)
+        x = plus_lane<0x141>(x);
+    if (G >= 16)
+        x = plus_lane<0x140>(x);
+    if (G >= 32) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+        const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+        x = halves(hi[0], lo[0]) + halves(hi[1], lo[1]);
+    }
+    if (G >= 64) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+        const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+        x = halves(hi[0], lo[0]) + halves(hi[1], lo[1]);
+    }
+    return x;
+}
 template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t x)
 {
     return group_all<G>(x, [](uint32_t p, uint32_t q) { return p > q ? p : q; });

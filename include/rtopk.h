@@ -505,9 +505,9 @@ size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hk
  *   q_out, k_out  as q and k, with strides of their own, rows apart from each
  *              other. An output may be its own input (the same address and strides);
  *              otherwise it overlaps no input and no other output
- * Norms and rotations are computed in float32, angles in float64; every output
- * is rounded once. D <= 256, (Hq+Hkv)*D <= 2^20, T <= 2^28 (else RTOPK_ENOTSUP);
- * eps finite, >= 0. Rows move as 16-byte vectors when D and rot are multiples of 32 bytes
+ * Norms and rotations are computed in float32 (a row whose squares leave its range is
+ * normalised in float64), angles in float64; every output is rounded once. D <= 256,
+ * (Hq+Hkv)*D <= 2^20, T <= 2^28 (else RTOPK_ENOTSUP); eps finite, >= 0. Rows move as 16-byte vectors when D and rot are multiples of 32 bytes
  * and all pointers and strides of 16, else element by element. Asynchronous on
  * `stream`; one launch, no workspace.
  */
