@@ -1,14 +1,20 @@
 // Internal interface between the host side (rtopk_filter.cpp) of filtered
-// sampling and its kernels (rtopk_filter.hip). Not part of the ABI.
+// sampling and its kernels (rtopk_filter.hip), and arithmetic of theirs that a plain
+// C++ compiler reads too, so that tests run it on the CPU. Not part of the ABI.
 #pragma once
 
+#include "rtopk_pages.h"
+
+#if !defined(RTOPK_ARITHMETIC_ONLY)
 #include "rtopk_internal.h"
+#endif
 
 namespace rtopk {
 
 constexpr int kFilterMaxV = 1 << 24; // 38 bits behind a weight's binary point
 constexpr int kFilterMaxR = 1 << 20; // a workgroup of 512 threads each: a launch counts its threads in 32 bits
 
+#if !defined(RTOPK_ARITHMETIC_ONLY)
 struct FilterArgs {
     const void *logits;  // [R][ld]
     int R, V;
@@ -20,6 +26,7 @@ struct FilterArgs {
     int32_t *out_token;
     float *out_logprob;
 };
+#endif
 
 // Weights are whole numbers, exp((x - max) / T) times 2^frac, the largest 2^frac: V of
 // them stay below 2^62, so that sums are exact and do not depend on their order.
@@ -29,6 +36,18 @@ constexpr int filter_frac(int V)
     while ((1ll << l) < V)
         ++l;
     return 62 - l < 50 ? 62 - l : 50;
+}
+
+// f times total, rounded down, or up: exact, where a double would drop the product's bits below
+// the 53rd and with them a border between two sums. f (by its float32 bits) is in [0, 1), so that it is
+// m 2^-(d + 32) with m < 2^32 and d >= 0; total <= 2^62. The product is high 2^32 + (lows mod 2^32).
+RTOPK_HD uint64_t part_of(uint32_t f, uint64_t total, bool up)
+{
+    const uint32_t e = f >> 23, m = (e ? (f & 0x7fffffu) | 0x800000u : f) << 8;
+    const int d = 126 - (int)(e ? e : 1u);
+    const uint64_t lows = m * (total & 0xffffffffu), high = m * (total >> 32) + (lows >> 32);
+    const uint64_t whole = d < 64 ? high >> d : 0;
+    return whole + (up && ((d < 64 ? whole << d : 0) != high || (uint32_t)lows != 0));
 }
 
 // Workgroups per row (1: no workspace is needed).
@@ -46,6 +65,8 @@ inline int filter_chunks(int R, int V)
     const int slots = 512 / R, c = slots < most ? slots : most; // two workgroups on each of 256 CUs
     return c < kFilterChunks ? c : kFilterChunks;
 }
+#if !defined(RTOPK_ARITHMETIC_ONLY)
 hipError_t launch_filter(const FilterArgs &a, int dtype, int chunks, void *ws, hipStream_t s);
+#endif
 
 } // namespace rtopk

@@ -345,20 +345,19 @@ template <int DT, bool SHORT> struct RowFilter {
         return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u);
     }
     static __device__ __forceinline__ int token_of(uint64_t o) { return (int)~(uint32_t)o; }
-    // u times S as a whole number below S
+    // u times S as a whole number below S; S is the same for every thread
     __device__ __forceinline__ uint64_t point(uint64_t S) const
     {
-        float u = a.u[row];
-        u = u > 0.f ? u : 0.f; // NaN: 0
-        const uint64_t g = u < 1.f ? (uint64_t)((double)u * (double)S) : S; // S > 0: the best is kept
-        return g < S ? g : S - 1;
+        const float u = a.u[row];
+        const uint32_t part = __float_as_uint(u > 0.f ? u : 0.f); // NaN: 0
+        S = of_lane(S, 0);
+        return u < 1.f || part == 0 ? part_of(part, S, false) : S - 1; // S > 0: the best is kept
     }
-    // What top-p asks of a beginning, of a weight of `total`
+    // What top-p (p < 1) asks of a beginning, of a weight of `total`
     __device__ __forceinline__ uint64_t goal_of(uint64_t total) const
     {
-        const double want = __builtin_ceil((double)p * (double)total);
-        const uint64_t g = want < 1. ? 1 : (uint64_t)want;
-        return g < total ? g : total;
+        const uint64_t g = part_of(__float_as_uint(p), total, true);
+        return g > 0 ? g : 1;
     }
     // The sum over the workgroup, for every thread.
     __device__ __forceinline__ uint64_t all_sum(uint64_t x)
@@ -535,8 +534,9 @@ template <int DT, bool SHORT> struct RowFilter {
             least_left = b.above_k > 0 ? b.above_k : 1; // (something is left)
             most_left = b.above_k + sh.value[3];
         }
-        find_weight(w, before, goal_of(least_left), 0);
-        find_weight(w, before, goal_of(most_left), 1);
+        const uint64_t goals = goal_of(lane & 1 ? most_left : least_left); // both at once: the code is long
+        find_weight(w, before, of_lane(goals, 0), 0);
+        find_weight(w, before, of_lane(goals, 1), 1);
         __syncthreads();
         b.p0 = sh.found[0];
         b.p1 = sh.found[1];

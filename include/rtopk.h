@@ -590,7 +590,7 @@ size_t rtopk_tree_attention_fp8_workspace_bytes(int B, int N, int Hq, int Hkv, i
  *   u          device [R] float32, held to [0, 1) (NaN is 0)
  *   out_token  device [R] int32; out_logprob device [R] float32
  * Weights are computed in 64 bits and summed as whole numbers of 2^-f, f = min(50,
- * 62 - ceil(log2 V)), so that sums are exact and the same call gives the same result;
+ * 62 - ceil(log2 V)), so that sums, and p and u times a sum, are exact and the same call gives the same result;
  * a candidate of weight below 2^-(f+1) is never drawn. The largest float32 counts as
  * infinite. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`. Few
  * long rows are cut over workgroups, which takes three launches and a workspace: the caller's, of
