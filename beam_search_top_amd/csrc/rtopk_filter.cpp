@@ -12,7 +12,7 @@ extern "C" size_t rtopk_sample_filtered_workspace_bytes(int R, int V)
 {
     if (R < 1 || V < 1 || V > rtopk::kFilterMaxV || R > rtopk::kFilterMaxR)
         return 0;
-    return rtopk::kWsFixedBytes + (rtopk::filter_chunks(R, V) > 1 ? R * rtopk::kFilterRowBytes : 0);
+    return rtopk::kWsFixedBytes + (rtopk::filter_chunks(R, V, false) > 1 ? R * rtopk::kFilterRowBytes : 0);
 }
 
 extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V, int64_t ld, const float *temperature,
@@ -57,7 +57,7 @@ extern "C" int rtopk_sample_filtered(const void *logits, int dtype, int R, int V
             return set_error(RTOPK_EHIP, "%s launch: %s", what, hipGetErrorString(e));
         return (int)RTOPK_OK;
     };
-    const int chunks = rtopk::filter_chunks(R, V);
+    const int chunks = rtopk::filter_chunks(R, V, top_k && !top_p);
     if (chunks > 1 && workspace)
         return go(chunks, (uint8_t *)workspace + rtopk::kWsFixedBytes);
     if (chunks > 1) {

@@ -53,14 +53,21 @@ RTOPK_HD uint64_t part_of(uint32_t f, uint64_t total, bool up)
 // Workgroups per row (1: no workspace is needed).
 constexpr int kFilterChunks = 64;
 constexpr size_t kFilterRowBytes = 49920; // workspace of a row that is cut
-inline int filter_chunks(int R, int V)
+// counts: top-k without top-p
+inline int filter_chunks(int R, int V, bool counts)
 {
     // Three launches and the workspace between them cost about 15 us whatever the size; a row's own workgroup takes
-    // 20 to 40 us per 40000 logits, and leaves CUs idle up to 256 rows. us cut / not: 1 x 16000 17 / 11, 16 x 24000
-    // 25 / 24, 64 x 24000 34 / 27; 1 x 28672 16 / 17, 32 x 32000 29 / 31, 64 x 40000 35 / 37, 128 x 32000 37 / 38,
-    // 128 x 100000 62 / 81, 8 x 250000 34 / 182; 200 x 40000 53 / 41, 256 x 100000 98 / 82.
+    // 20 to 40 us per 40000 logits, and leaves CUs idle up to 256 rows. us cut / not, bfloat16, every filter: 1 x 16000
+    // 17 / 11, 16 x 24000 25 / 24, 64 x 24000 34 / 27; 1 x 28672 16 / 17, 32 x 32000 29 / 31, 64 x 40000 35 / 37,
+    // 128 x 32000 37 / 38, 128 x 100000 62 / 81, 8 x 250000 34 / 182. With 129 to 170 rows, of three chunks each, it pays from
+    // longer rows on: 160 x 60000 56 / 55, 160 x 70000 62 / 61, 160 x 80000 66 / 70, 160 x 150000 101 / 140, 170 x 250000
+    // 150 / 189 (top-p alone 57 / 59, 57 / 62, 61 / 81, 92 / 141, 135 / 192); with two chunks it does not: 200 x 60000 69 / 56,
+    // 200 x 100000 99 / 89, 200 x 250000 206 / 190, 256 x 100000 99 / 83.
+    // Top-k alone weighs only what it keeps, and a row's own workgroup takes half as long: 1 x 30000 17 / 15,
+    // 8 x 30000 20 / 18, 8 x 60000 21 / 26, 32 x 30000 22 / 18, 32 x 60000 26 / 27, 64 x 60000 29 / 27, 64 x 100000 35 / 38,
+    // 96 x 100000 41 / 39, 128 x 100000 46 / 39, 128 x 250000 86 / 90, 160 x 250000 105 / 91.
     const int most = V / 4096;
-    if (R > 128 || most < 7)
+    if (R > 170 || most < 7 || (R > 128 && (counts || V < 1 << 16)) || (counts && V < 1024 * (R + 32)))
         return 1;
     const int slots = 512 / R, c = slots < most ? slots : most; // two workgroups on each of 256 CUs
     return c < kFilterChunks ? c : kFilterChunks;

@@ -168,3 +168,14 @@ def test_every_code_and_scale_as_a_key(N, D, dt):
         # the score in base 2 and back: four roundings of it, and one of a number up to 11 above it (lse's reference)
         off = (lse.double() - want).abs() <= 4 * 2.0 ** -24 * want.abs() + 2 * 2.0 ** -24 * (want.abs() + 16)
         assert off[see].all(), (e, float((lse.double() - want).abs()[see].max()))
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("R,V", [(129, 65536), (170, 70001), (171, 70001), (66, 100352), (67, 100352), (3, 35839), (3, 35840)])
+def test_rows_at_the_limits_of_the_cut(R, V, dt):
+    x, rng = _rows(R, V, dt, seed=R, sigma=2.0)
+    u = rng.random(R)
+    for kw in (dict(k=50), dict(k=3000, m=0.01), dict(p=0.9), dict(k=50, p=0.95, m=0.02, t=0.9), dict()):
+        tok, lp = _both_forms(x, u, str(kw), oracle=False, **kw)
+        some = [0, R // 2, R - 1]
+        assert _check(x[some].contiguous(), u[some], str(kw), **kw) == ([tok[r] for r in some], [lp[r] for r in some])

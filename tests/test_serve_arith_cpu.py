@@ -24,7 +24,7 @@ def arith(tmp_path_factory):
 #include <string.h>
 using namespace rtopk;
 extern "C" unsigned long long part_(float f, unsigned long long t, int up) { uint32_t b; memcpy(&b, &f, 4); return part_of(b, t, up); }
-extern "C" int chunks_(int R, int V) { return filter_chunks(R, V); }
+extern "C" int chunks_(int R, int V, int counts) { return filter_chunks(R, V, counts); }
 extern "C" int frac_(int V) { return filter_frac(V); }
 ''')
     so = d / "filter.so"
@@ -56,3 +56,17 @@ def test_parts_of_a_sum_are_exact(arith):
 def test_weights_of_a_row_sum_below_two_to_the_62(arith):
     for V in (1, 2, 4096, 4097, 250000, 2 ** 24 - 1, 2 ** 24):
         assert V << arith.frac_(V) <= 2 ** 62
+
+
+def test_where_rows_are_cut(arith):
+    # a workspace has room for the call whatever its filters; chunks fill the GPU and are not idle
+    for R in list(range(1, 300)) + [512, 4096, 2 ** 20]:
+        need = rtopk.rtopk_sample_filtered_workspace_bytes
+        for V in (1, 4096, 28671, 28672, 33791, 33792, 40000, 65535, 65536, 100000, 163840, 250000, 2 ** 24):
+            c, k = arith.chunks_(R, V, 0), arith.chunks_(R, V, 1)
+            assert k in (1, c) and 1 <= c <= 64 and (c == 1 or (R * c <= 512 and V // c >= 4096))
+            assert need(R, V) == (need(R, 1) if c == 1 else need(R, 1) + R * 49920)
+    # rows of 100000 and more are cut up to where three chunks of each fill the GPU
+    assert [arith.chunks_(R, 100000, 0) for R in (1, 8, 128, 129, 170, 171, 256)] == [24, 24, 4, 3, 3, 1, 1]
+    assert [arith.chunks_(R, 65535, 0) for R in (128, 129)] == [4, 1]
+    assert [arith.chunks_(R, 100000, 1) for R in (1, 65, 66, 129)] == [24, 7, 1, 1]
