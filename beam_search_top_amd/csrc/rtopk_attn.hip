@@ -871,11 +871,11 @@ __global__ __launch_bounds__(64 * WR, DP > 128 || (WR < 4 && DP > 64) ? 1 : 2) v
 // The kernel of few rows (at most 16 NB per key head): a step of decoding, a
 // small tree. It is bound by reading keys and values once, so what counts is
 // bytes in flight, whole lines per load and even shares: every wave takes
-// steps of 32 keys of its own, loads whole rows to registers, and refills the
+// steps of 32 keys (few_step) of its own, loads whole rows to registers, and refills the
 // key registers as soon as the keys are in LDS and the value registers as soon
 // as the outputs are made, without a barrier in the loop (the LDS that turns
-// key rows into operands is the wave's own). All loads are non-temporal:
-// nobody reads the data again. One row over 90000 and 131000 keys, 8 key heads
+// key rows into operands is the wave's own). Loads are non-temporal, for
+// nobody reads the data again, but where a row is half a line (fetch_row). One row over 90000 and 131000 keys, 8 key heads
 // of 128, bf16 (0.9 GB): 156 us, 5.8 TB/s, where a plain read reaches 7.0; in
 // pieces of 64 bytes, as the operands want the keys, and without equal shares
 // 200 us. 128 x 4 rows over 130-512 keys, 16 heads of 64 (0.17 GB): 33 us.
@@ -1067,15 +1067,15 @@ __global__ __launch_bounds__(64 * kFewWaves, few_waves(DP, NB, MODE)) void attn_
     gchar *kbase = (gchar *)a.k + kElemBytes * (TREE ? hk * a.ks[2] : b * a.ks[0] + hk * a.ks[2]);
     gchar *vbase = (gchar *)a.v + kElemBytes * (TREE ? hk * a.vs[2] : b * a.vs[0] + hk * a.vs[2]);
     uint8_t *mine = smem + wave * kFewStep * ROWB;
-    // Step t is rows first(t) ... + 31. Past the last row that can be read (cross: S
-    // >= 32) it begins earlier and leaves out the keys of the step before.
+    // Step t is kFewStep rows from first(t) on. Past the last row that can be read (cross, steps of
+    // 32: S >= 32) it begins earlier and leaves out the keys of the step before.
     auto first = [&](int t) -> int {
         if (TREE)
             return t * kFewStep;
         const int f = (t < t_end ? t : t_begin) * kFewStep;
         return f < a.S - kFewStep ? f : a.S - kFewStep;
     };
-    // what decides about key first(t) + lane mod 32, read ahead: its page, or its mask
+    // what decides about key first(t) + lane mod kFewStep, read ahead: its page, or its mask
     auto fetch = [&](int t) -> int {
         const int j = first(t) + (lane & (kFewStep - 1));
         if (t >= t_end || j >= kr.end)
@@ -1110,8 +1110,8 @@ __global__ __launch_bounds__(64 * kFewWaves, few_waves(DP, NB, MODE)) void attn_
     };
     // Row u + lane_r of a step (u the same for the wave) lies at a base of the wave's and a
     // 32-bit offset of the lane's: cross attention's rows are evenly spaced (the
-    // host sees to it that 32 of them span less than 2^32 bytes), up to 8 rows of a tree lie on
-    // one page where pages allow it. Else every lane has a 64-bit offset of its own.
+    // host sees to it that 32 of them span less than 2^32 bytes), the rows of one load of a tree (8; of
+    // 64 codes 16) lie on one page where pages allow it. Else every lane has a 64-bit offset of its own.
     const int lrow = lane / CH, lchunk = lane % CH;
     constexpr int CE = 16 / kElemBytes; // elements of a chunk
     const uint32_t kstep = kElemBytes * (uint32_t)a.ks[1], vstep = kElemBytes * (uint32_t)a.vs[1];

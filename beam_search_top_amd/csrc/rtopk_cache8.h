@@ -41,7 +41,7 @@ RTOPK_HD float stored_limit(int dtype) { return dtype == 1 ? 61440.f : 0x1.ep127
 
 // Tokens per workgroup of the rotation, of `row` elements each: enough to fill its lanes
 // a few times, and more where T tokens would take 2^24 workgroups of 256 threads. Their
-// sines and cosines fit in LDS: at most kMaxRopeTokens / 2^24 = 16 tokens.
+// sines and cosines fit in LDS: at most 17 tokens (kMaxRopeTokens over 2^24 - 1, rounded up) of 128.
 constexpr int64_t kMaxRopeTokens = (int64_t)1 << 28;
 inline int rope_tokens(int64_t T, int64_t row)
 {

@@ -254,7 +254,8 @@ AttnPlan plan_attention(int B, int N, int Hq, int Hkv, int D, int S, bool wide, 
         // cut: 34 us, cut in two or more 44 us, for the ends of every share cost more
         // than the balance gains. 8 bits: not cut up to two steps per wave, where shares and their join cost more
         // (8 requests, 16 heads of 64 / 8 of 128: kernel 8.8 / 8.0 us uncut and 9.4 / 9.5 cut at 500 / 250 keys, 12.7 / 10.9
-        // uncut and 10.3 / 9.9 cut at twice as many).
+        // uncut and 10.3 / 9.9 cut at twice as many). The rule sees what a table's row holds, for the lengths are on the
+        // device: short requests under a wide table are cut.
         p.bn = fp8 && p.dp == 64 ? 64 : 32; // few_step
         p.waves = 4;
         p.row_tiles = 1;
