@@ -147,9 +147,9 @@ constexpr Borders kNoBorders{kBins, kBins, -1, kBins, 0, 0, 0, 0};
 // What keeps everything but -infinity.
 constexpr uint64_t kKeepAll = 0x00800000ull << 32;
 
-// One row and what its filters are. SHORT: the loop over the logits of 16 bytes is not unrolled. A
-// launch of few rows meets its code for the first time everywhere (about 80 ns for each 64 bytes of
-// it), which costs more than the loop (the last launch of 8 x 250000: 31 us with unrolled loops, 26 without).
+// One row and what its filters are. SHORT: the loop over the logits of 16 bytes is not unrolled. A lane of a
+// launch of few rows has one or two pieces, for which unrolled code takes as long (the last launch of 8 x 250000: 19.8
+// us, 19.2 as it is; of 32 x 32000 15.8 both) and is more to fetch for a call that finds it nowhere.
 template <int DT, bool SHORT> struct RowFilter {
     typedef Logit<DT> L;
     typedef typename L::Raw Raw;
@@ -899,9 +899,9 @@ template <int DT, bool SHORT> struct RowFilter {
 //      with too many equal or nearly equal ones finds it by the bits of the logits.
 //   5. Kept weights are summed by runs of the row, and the run that the draw falls in is read again.
 // 512 rows of 40000, float16, 54 us, two rows to a CU. Bound by the rows that have top-p alone and
-// keep more than a list holds: two passes of 25 to 30 vector instructions per logit, 13 us of issue for two rows and
-// 18 to 20 measured; alone on its CU a row's pass takes 11.5 and half of its time is waiting. Such a row takes 52 us,
-// one with top-k 25 (its count, 6, waits for LDS). A list of twice the length would save nothing: making and reading it
+// keep more than a list holds: two passes of 25 to 30 vector instructions per logit, 13 us of issue for two rows by
+// their number, and 17 to 23 by stamps; alone on its CU a row's passes take 12 and 17, and half of all wave time is
+// waiting. Such a row takes 52 us, one with top-k 23 (its count, 6, waits for LDS). A list of twice the length would save nothing: making and reading it
 // takes 15 us, a whole pass 17. Loads three pieces ahead spill (63 us), and 1024 threads leave one row to a CU (69 us;
 // with 200 rows 40 against 41).
 template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(const FilterArgs a)
@@ -948,8 +948,9 @@ template <int DT> __global__ __launch_bounds__(kFThreads, 4) void filter_row(con
 
 // ---- few rows: each cut into `chunks` of whole runs, a workgroup each, in three launches that pass
 // histograms, sums and zones through the workspace. 8 rows of 250000, bfloat16, 33 us: 3, 9 and 19 of the launches and
-// their gaps; 32 rows of 32000, float32, 25.6. Bound by chains of round trips (ends, histograms, ticket, runs, the
-// drawn run) and by code that every workgroup fetches cold.
+// their gaps; 32 rows of 32000, float32, 25.6. Bound by a chain of short steps that wait for each other, 0.5 to 4 us each
+// by stamps: in the last launch ends and histograms 2.3, borders 2.1 and 2.4, weights 3.4, runs, ticket and their reading
+// 2.3, the zone's order 4.4, the drawn run 2.0. Instruction fetches miss in 1 to 2 of 100.
 struct alignas(256) SplitRow {
     uint64_t w[kBins], runs[kBins], zone[kZone];
     uint32_t n[kBins];

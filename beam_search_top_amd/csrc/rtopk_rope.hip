@@ -27,7 +27,7 @@ constexpr int kRopeThreads = 256;
 // An angle is the product of the position and the frequency in 64 bits, taken off
 // whole turns there: position 10^6 at frequency 1 would lose 2^-4 of a radian in 32 bits.
 //
-// Bound by HBM: 60001 tokens of 32 + 8 heads of 128, bfloat16 with norms, 243 us, 4.97 TB/s read and
+// Bound by HBM: 60001 tokens of 32 + 8 heads of 128, bfloat16 with norms, 245 us, 4.93 TB/s read and
 // written (a device copy: 5.01). 200 tokens of 16 + 16 heads of 64 take 4.0 us, a chain of a position, an
 // angle and a row; the call on the host takes 8.8.
 template <int DT, int VE, int LPH>
