@@ -507,9 +507,9 @@ size_t rtopk_cross_attention_workspace_bytes(int B, int N, int S, int Hq, int Hk
  *              otherwise it overlaps no input and no other output
  * Norms and rotations are computed in float32 (a row whose squares leave its range is
  * normalised in float64), angles in float64; every output is rounded once. D <= 256,
- * (Hq+Hkv)*D <= 2^20, T <= 2^28 (else RTOPK_ENOTSUP); eps finite, >= 0. Rows move as 16-byte vectors when D and rot are multiples of 32 bytes
- * and all pointers and strides of 16, else element by element. Asynchronous on
- * `stream`; one launch, no workspace.
+ * (Hq+Hkv)*D <= 2^20, T <= 2^28 (else RTOPK_ENOTSUP); eps finite, >= 0. Rows move as
+ * 16-byte vectors when D and rot are multiples of 32 bytes and all pointers and strides
+ * of 16, else element by element. Asynchronous on `stream`; one launch, no workspace.
  */
 int rtopk_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, int dtype,
                        const int32_t *positions, const float *freqs, int rot, int interleaved, const void *q_weight,
@@ -590,9 +590,9 @@ size_t rtopk_tree_attention_fp8_workspace_bytes(int B, int N, int Hq, int Hkv, i
  *   u          device [R] float32, held to [0, 1) (NaN is 0)
  *   out_token  device [R] int32; out_logprob device [R] float32
  * Weights are computed in 64 bits and summed as whole numbers of 2^-f, f = min(50,
- * 62 - ceil(log2 V)), so that sums, and p and u times a sum, are exact and the same call gives the same result;
- * a candidate of weight below 2^-(f+1) is never drawn. The largest float32 counts as
- * infinite. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`. Few
+ * 62 - ceil(log2 V)), so that sums, and p and u times a sum, are exact and the same call
+ * gives the same result; a candidate of weight below 2^-(f+1) is never drawn. The largest
+ * float32 counts as infinite. V <= 2^24, R <= 2^20 (else RTOPK_ENOTSUP). Asynchronous on `stream`. Few
  * long rows are cut over workgroups, which takes three launches and a workspace: the caller's, of
  * ws_bytes >= rtopk_sample_filtered_workspace_bytes(...) bytes and 256-byte aligned (it needs no
  * filling; calls sharing it must be ordered), or with NULL the library-owned one that
